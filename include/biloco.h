@@ -262,6 +262,87 @@ int biloco_gemm_noalloc(const void *x_bf16, const uint8_t *W_fp4, const uint8_t 
                         biloco_stream_t stream);
 
 /*
+ * ---- FP8 block format -----------------------------------------------------
+ * The layers of a model that stay at 8 bits next to the NVFP4 ones, and the steps
+ * between them.  The BiLoCo pages have no counterpart of these calls.
+ *
+ * Format: E4M3 codes (sign, 4 exponent, 3 mantissa bits; 0x7F and 0xFF are NaN) with
+ * one FP32 scale per 128 elements of a row (activations) or per 128 x 128 tile
+ * (weights); the last block of a row, or tile, may be smaller.
+ *     a = max(max |v| over the block, 2^-100)
+ *     scale = RN(a / 448),  code = E4M3(RN(v * RN(448 / a)))
+ * in FP32, E4M3 to nearest-even with saturation at 448.  A NaN makes its whole block
+ * NaN; an infinity makes the block's scale infinite (and its values NaN).
+ *
+ * Types of a floating array where a call takes more than one:
+ */
+enum { BILOCO_TYPE_BF16 = 0, BILOCO_TYPE_F32 = 1 };
+
+/*
+ * biloco_fp8_quant_act - BF16 activation -> FP8 blocks.
+ *   x_bf16  [M][K] bfloat16, row stride ldx elements, 16-byte aligned; ldx % 8 == 0
+ *   M, K    M >= 0 (0: nothing is done), K >= 16, K % 16 == 0
+ *   codes   out [M][K] E4M3 bytes, 16-byte aligned
+ *   scales  out [ceil(K/128)][M] float (block-major: one token's scales are M apart)
+ */
+int biloco_fp8_quant_act(const void *x_bf16, long long ldx, int M, int K, uint8_t *codes,
+                         float *scales, biloco_stream_t stream);
+
+/*
+ * biloco_fp8_pack_weight - E weights of [N][K] (contiguous, BF16 or FP32) -> FP8 tiles.
+ *   codes   out [E][N][K] E4M3 bytes
+ *   scales  out [E][ceil(N/128)][ceil(K/128)] float
+ * K % 16 == 0; W and codes 16-byte aligned.  Tiles do not cross weights.
+ */
+int biloco_fp8_pack_weight(const void *W, int w_type, int E, int N, int K, uint8_t *codes,
+                           float *scales, biloco_stream_t stream);
+
+/*
+ * biloco_fp8_gemm - y[m,n] = sum_b xs[b,m] ws[n/128,b] sum_{k in block b} x[m,k] w[n,k].
+ *   x_codes [M][K], x_scales [ceil(K/128)][M]   as written by biloco_fp8_quant_act
+ *   w_codes [N][K], w_scales [ceil(N/128)][ceil(K/128)]  as by biloco_fp8_pack_weight
+ *   y       out [M][N], BF16 (2-byte aligned) or FP32 (4-byte aligned) by y_type
+ *   limits  0 <= M <= 2^24 (0: nothing is done), 1 <= N <= 2^24, K % 16 == 0,
+ *           16 <= K <= 2^24; codes 16-byte aligned
+ * Any batch size runs one kernel, which keeps no scratch and shares nothing between
+ * calls: calls on different streams, and graphs replayed at once, do not disturb each
+ * other.  Sums are FP32; the result depends only on the operands and the shape.
+ * The kernel is launched with programmatic dependent launch and reads w_codes before it
+ * waits for the kernel before it (see biloco_gemm on what must not write the weight).
+ * A bounded wait that expires inside the kernel is reported by biloco_last_error, on
+ * whichever stream asks first; y is then not valid.
+ */
+int biloco_fp8_gemm(const uint8_t *x_codes, const float *x_scales, const uint8_t *w_codes,
+                    const float *w_scales, void *y, int y_type, int M, int N, int K,
+                    biloco_stream_t stream);
+
+/*
+ * biloco_block_norm - the step between two blocks of a layer, in one pass:
+ *     u  = y rsqrt(mean(y^2) + eps) (post_weight + offset)     (u = y without post_weight)
+ *     h' = res_scale h + gate u
+ *     x  = h' rsqrt(mean(h'^2) + eps) (pre_weight + offset)
+ *   y_bf16       [M][D] bfloat16 output of the block, row stride ldy; NULL: no block
+ *                before (u = 0, no post_weight, no gate)
+ *   h            [M][D] residual stream of type h_type, row stride ldh; NULL: none yet
+ *   post_weight, pre_weight   [D] of type w_type, NULL: no norm after / before
+ *   gate         [gate_rows][D] of gate_type, row m takes row m / (M / gate_rows)
+ *                (M % gate_rows == 0); NULL: 1
+ *   h_out        out [M][D] of type h_type, row stride ldho; may be h itself, or NULL
+ *   x_bf16       out [M][D] bfloat16, or NULL
+ *   codes,scales out x as FP8 blocks (D % 16 == 0), layout of biloco_fp8_quant_act, or NULL
+ * h' enters x unrounded, and x the FP8 blocks unrounded: each output is rounded once.
+ * limits: M >= 0, 8 <= D <= BILOCO_NORM_MAX_D, D % 8 == 0, row strides >= D and multiples of 8
+ * elements, 16-byte aligned arrays.  Outputs must not overlap inputs other than h_out = h
+ * with the same stride.
+ */
+#define BILOCO_NORM_MAX_D 32768
+int biloco_block_norm(const void *y_bf16, long long ldy, const void *h, long long ldh, int h_type,
+                      const void *post_weight, const void *pre_weight, int w_type,
+                      const void *gate, int gate_type, int gate_rows, float res_scale,
+                      float offset, float eps, int M, int D, void *h_out, long long ldho,
+                      void *x_bf16, uint8_t *codes, float *scales, biloco_stream_t stream);
+
+/*
  * Launch form of the GEMM kernels for later biloco_gemm / biloco_gemm_noalloc
  * calls (process-wide), a combination of:
  *   BILOCO_LAUNCH_PDL          programmatic dependent launch: the kernel may start

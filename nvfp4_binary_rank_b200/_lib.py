@@ -29,6 +29,8 @@ _lock = threading.Lock()
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_longlong
+_F = ctypes.c_float
 
 # name -> (restype, argtypes); must match include/biloco.h
 SIGNATURES = {
@@ -40,6 +42,10 @@ SIGNATURES = {
     "biloco_decompose": (_I, [_P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "biloco_gemm": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
     "biloco_gemm_noalloc": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
+    "biloco_fp8_quant_act": (_I, [_P, _L, _I, _I, _P, _P, _P]),
+    "biloco_fp8_pack_weight": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
+    "biloco_fp8_gemm": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
+    "biloco_block_norm": (_I, [_P, _L, _P, _L, _I, _P, _P, _I, _P, _I, _I, _F, _F, _F, _I, _I, _P, _L, _P, _P, _P, _P]),
     "biloco_set_mode": (_I, [_I]),
     "biloco_resolve_mode": (_I, [_I, _I, _I, _I]),
     "biloco_last_error": (_I, [_P]),

@@ -27,26 +27,6 @@ size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-int check_device() {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return BILOCO_ERR_CUDA;
-  static std::mutex mu;
-  static std::vector<int> ok_devices, bad_devices;
-  std::lock_guard<std::mutex> lk(mu);
-  if (std::find(ok_devices.begin(), ok_devices.end(), dev) != ok_devices.end()) return BILOCO_OK;
-  if (std::find(bad_devices.begin(), bad_devices.end(), dev) != bad_devices.end())
-    return BILOCO_ERR_DEVICE;
-  int major = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
-    return BILOCO_ERR_CUDA;
-  if (major != 10) {
-    bad_devices.push_back(dev);
-    return BILOCO_ERR_DEVICE;
-  }
-  ok_devices.push_back(dev);
-  return BILOCO_OK;
-}
-
 // Region offsets of one scratch block, every region 256-byte aligned.
 struct Carve {
   size_t status, counters, act_fp4, act_sf, zpart, zfin, slots, total;
@@ -102,6 +82,26 @@ void apply_carve(Scratch& s, const Carve& c, const ScratchNeed& n) {
 }
 
 }  // namespace
+
+int check_device() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return BILOCO_ERR_CUDA;
+  static std::mutex mu;
+  static std::vector<int> ok_devices, bad_devices;
+  std::lock_guard<std::mutex> lk(mu);
+  if (std::find(ok_devices.begin(), ok_devices.end(), dev) != ok_devices.end()) return BILOCO_OK;
+  if (std::find(bad_devices.begin(), bad_devices.end(), dev) != bad_devices.end())
+    return BILOCO_ERR_DEVICE;
+  int major = 0;
+  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
+    return BILOCO_ERR_CUDA;
+  if (major != 10) {
+    bad_devices.push_back(dev);
+    return BILOCO_ERR_DEVICE;
+  }
+  ok_devices.push_back(dev);
+  return BILOCO_OK;
+}
 
 int num_sms() {
   int dev = 0, n = 148;
@@ -312,7 +312,8 @@ int biloco_last_error(biloco_stream_t stream) {
     }
   }
   const int static_status = noalloc_take_status();
-  return status != 0 ? status : static_status;
+  const int fp8_status = fp8_take_status(s);
+  return status != 0 ? status : static_status != 0 ? static_status : fp8_status;
 }
 
 const char* biloco_status_string(int status) {

@@ -45,7 +45,8 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// 2-D byte tensor [rows][inner_bytes], box [box_rows][128 B], 128-byte swizzle.
+}  // namespace
+
 bool make_tmap(CUtensorMap* m, const void* base, uint64_t inner_bytes, uint64_t rows, uint32_t box_rows) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return false;
@@ -57,6 +58,8 @@ bool make_tmap(CUtensorMap* m, const void* base, uint64_t inner_bytes, uint64_t 
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+
+namespace {
 
 // 2-D tensor without swizzle: [rows][inner elements of elem_bytes], box [box_rows][box_inner].
 bool make_tmap_plain(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint32_t elem_bytes,

@@ -3,6 +3,7 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "launch_common.h"
@@ -35,6 +36,15 @@ struct ScratchNeed {
 Scratch* get_scratch(cudaStream_t stream, const ScratchNeed& need);
 
 int num_sms();
+
+// BILOCO_OK, or an error where the current device is not an sm_100 GPU.
+int check_device();
+
+// Tensor map of a 2-D byte tensor [rows][inner_bytes], box [box_rows][128 B], 128-byte swizzle.
+bool make_tmap(CUtensorMap* m, const void* base, uint64_t inner_bytes, uint64_t rows, uint32_t box_rows);
+
+// Status word of the FP8 GEMM on the current device: read on `s`, returned and cleared (synchronous).
+int fp8_take_status(cudaStream_t s);
 
 // Launchers (return cudaError_t values).
 cudaError_t launch_quant_act_rowmajor(const uint16_t* x, int M, int K, uint8_t* codes, uint8_t* sf,
