@@ -3,18 +3,24 @@
 //   y[m,n] = sum_b sx[b,m] * sw[n/128,b] * sum_{k in block b} xq[m,k] wq[n,k]
 //
 // Each block's inner sum runs on the tensor cores (tcgen05.mma kind::f8f6f4, four K = 32
-// steps) into one of two TMEM accumulators; the promoting warps read it back, multiply
-// it by the two scales and add it to FP32 sums in registers while the next block is
-// being multiplied into the other accumulator.  Block sums and the running sums are
+// steps) into one of several TMEM accumulators; the promoting warps read it back, multiply
+// it by the two scales and add it to FP32 sums in registers while the next blocks are
+// being multiplied into the other accumulators.  Block sums and the running sums are
 // FP32; y is rounded once.
 //
 // Two forms of one kernel:
-//   rows form (more than 128 tokens): the MMA's 128 rows are tokens and its columns weight
+//   rows form (more than 128 tokens): the MMA's rows are tokens and its columns weight
 //     rows, so a thread's scale is one number per block (its token's times its 128
-//     columns').  Persistent over tiles; bound by the tensor cores.
+//     columns').  A pair of CTAs (cta_group::2) computes 256 tokens x 256 weight rows, each
+//     CTA loading 128 rows of either operand: 32 KB per block and SM instead of 48.
+//     Persistent over tiles.
 //   swapped form (up to 128 tokens): the MMA's 128 rows are weight rows and its columns
-//     tokens, so a decode batch is not padded to 128 rows; scales vary over the columns
-//     and come through shared memory.  Bound by reading the weight.
+//     tokens, so a decode batch is not padded to 128 rows; scales vary over the columns.
+//     Bound by reading the weight.
+// The token scales come through a ring in shared memory that a warp of its own fills a few
+// blocks ahead: loaded by the promoting warps themselves, one block ahead, their latency
+// (about 1000 clocks under load) set the pace of the rows form.
+//
 // Where there are fewer tiles than CTA slots, a cluster of up to 8 CTAs splits K: each
 // leaves its FP32 sums in its own shared memory and the cluster adds them in rank order
 // over distributed shared memory, so the result does not depend on timing and no
@@ -29,6 +35,7 @@
 #include "../../include/biloco.h"
 #include "fp8_dev.cuh"
 #include "fp8_ops.h"
+#include "fp8_promote.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -46,21 +53,71 @@ struct Fp8GemmParams {
   int tiles_a, tiles_b;  // tiles along the MMA's rows and columns
   int split;             // CTAs of the cluster that splits K
   int y_f32;
-  int vec;               // bytes of the widest aligned store of a y row: 32, 16, 8, 4 or 2
+  int vec;               // bytes of the widest aligned store of a y row: 32, 16, 8 or 2
 };
 
-// D(tmem) (+)= A(smem) * B(smem)^T, E4M3 operands, FP32 accumulation, M = 128, K = 32.
+// D(tmem) (+)= A(smem) * B(smem)^T, E4M3 operands, FP32 accumulation, K = 32; M = 128 in
+// one CTA, or M = 256 over a pair (each CTA's 128 rows of A and half of B's rows).
+template <bool kPair>
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, SmemDesc a, SmemDesc b, uint32_t idesc,
                                           uint32_t accumulate) {
+  if constexpr (kPair)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %2};\n\t"
+        "mov.b64 db, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], da, db, %5, p;\n\t"
+        "}" ::"r"(d_tmem),
+        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, %2};\n\t"
+        "mov.b64 db, {%3, %4};\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n\t"
+        "}" ::"r"(d_tmem),
+        "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrive on the barrier at this offset in every CTA of `mask` once the MMAs issued so far are done.
+__device__ __forceinline__ void tc_commit_pair(uint32_t bar, uint16_t mask) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
-      "mov.b64 da, {%1, %2};\n\t"
-      "mov.b64 db, {%3, %4};\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n\t"
-      "}" ::"r"(d_tmem),
-      "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(accumulate)
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"(mask)
       : "memory");
+}
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// TMA load into this CTA's shared memory, counted on a barrier of either CTA of the pair.
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* m, uint32_t bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+// Arrive on a barrier of another CTA of the cluster (a mapa address).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// One lane of a converged warp.  The compiler knows that a branch on it leaves a single
+// thread, so the operands of tcgen05 and TMA instructions go to uniform registers
+// directly; after a branch on `lane == 0` each of them cost about 130 clocks.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -76,24 +133,40 @@ __device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ float ld_dsmem(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr));
+__device__ __forceinline__ float4 ld_dsmem4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
   return v;
 }
 
 template <bool kSwap, int kBN>
 struct Cfg {
-  static constexpr int kGroups = kBN > 128 ? 2 : 1;            // promoting warpgroups
+  static constexpr int kPair = kSwap ? 1 : 2;                  // CTAs of one MMA
+  static constexpr int kGroups = !kSwap ? 4 : kBN >= 64 ? 2 : 1;            // promoting warpgroups
+  static constexpr int kWarps = 4 * kGroups;                   // promoting warps
   static constexpr int kCols = kBN / kGroups;                  // columns per promoting thread
   static constexpr int kThreads = 128 + 128 * kGroups;
   static constexpr int kCtasPerSm = (kSwap && kBN <= 64) ? 2 : 1;
-  static constexpr int kStageBytes = 16384 + kBN * 128;
-  static constexpr int kStages = kSwap ? (kBN <= 16 ? 6 : kBN <= 32 ? 5 : kBN <= 64 ? 4 : 6) : (kBN > 128 ? 4 : 6);
+  static constexpr int kStageBytes = 16384 + (kSwap ? kBN * 128 : 16384);
+  static constexpr int kStages = kSwap ? (kBN <= 16 ? 6 : kBN <= 32 ? 5 : kBN <= 64 ? 4 : 6) : 6;
   static constexpr int kSmem = kStages * kStageBytes + 1024;   // slack for the 1024-byte alignment
-  static constexpr uint32_t kTmemCols = 2 * kBN < 32 ? 32 : 2 * kBN;
+  // Accumulators in TMEM.  In the rows form each promoting warpgroup has its own 128
+  // columns of the tile and two accumulators for them: with one accumulator pair of 256
+  // columns, the chain multiply - read back - release set the pace (1200 clocks a block).
+  static constexpr int kHalves = kSwap ? 1 : 2;
+  static constexpr int kN = kBN / kHalves;                     // columns of one MMA
+  static constexpr int kBufs = kSwap ? 4 : 2;
+  static constexpr uint32_t kTmemCols = kBufs * kBN;
+  static constexpr int kTok = kSwap ? kBN : 128;               // token scales per block
+  static constexpr int kRing = kStages + kBufs;                // blocks of scales (see the scale warp)
+  // rows form: registers of a promoting thread and of the others (setmaxnreg)
+  static constexpr int kRegLaunch = 96, kRegPromote = 104, kRegOther = 64;
+  static constexpr int kRegTotal = 128 * kGroups * kRegPromote + 128 * kRegOther;
   static constexpr int kPitch = kSwap ? 128 : kBN + 4;         // floats per row of the split-K exchange
   static_assert(kStages * kStageBytes >= (kSwap ? kBN : 128) * kPitch * 4, "the exchange reuses the stages");
+  // a stage's "done" phase must be seen by the promoting warps before the next one ends
+  static_assert(kSwap || kRegTotal <= kThreads * kRegLaunch, "");
+  static_assert(kBufs <= kStages && kTmemCols * kCtasPerSm <= 512, "");
 };
 
 // The tile t of a persistent walk: groups of eight row tiles, column tiles inside, so
@@ -152,195 +225,338 @@ __device__ __forceinline__ void store_one(const Fp8GemmParams& p, long long at, 
     static_cast<uint16_t*>(p.y)[at] = static_cast<uint16_t>(bf16x2_from_f32(v, 0.0f));
 }
 
+// Stores four consecutive y values of one row (fewer at the row's end).
+__device__ __forceinline__ void store4(const Fp8GemmParams& p, long long at, int n_left, const float* v) {
+  if (p.y_f32 && p.vec >= 16) {
+    *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) = make_float4(v[0], v[1], v[2], v[3]);
+  } else if (!p.y_f32 && p.vec >= 8) {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + at) =
+        make_uint2(bf16x2_from_f32(v[0], v[1]), bf16x2_from_f32(v[2], v[3]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (j < n_left) store_one(p, at + j, v[j]);
+  }
+}
+
 template <bool kSwap, int kBN>
 __global__ void __launch_bounds__(Cfg<kSwap, kBN>::kThreads, Cfg<kSwap, kBN>::kCtasPerSm)
 fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const Fp8GemmParams p) {
   using C = Cfg<kSwap, kBN>;
+  constexpr bool kPair = C::kPair == 2;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * C::kStages + 4];
-  __shared__ __align__(16) float col_scale[2][kSwap ? kBN : 4];
+  __shared__ __align__(8) uint64_t bars[(1 + C::kHalves) * C::kStages + C::kHalves * C::kBufs];
+  __shared__ __align__(16) float ring[C::kRing][C::kTok + 4];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  const uint32_t full0 = smem_u32(bars), empty0 = full0 + 8 * C::kStages;
-  const uint32_t tfull0 = empty0 + 8 * C::kStages, tempty0 = tfull0 + 16;
+  const uint32_t full0 = smem_u32(bars), done0 = full0 + 8 * C::kStages;
+  const uint32_t tempty0 = done0 + 8 * C::kHalves * C::kStages;
 
+  const int crank = kPair || p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int half = kPair ? crank & 1 : 0;              // which CTA of the pair
   if (warp == 0 && lane == 0) {
     prefetch_tmap(&tm_a);
     prefetch_tmap(&tm_b);
     for (int i = 0; i < C::kStages; ++i) {
       mbar_init(full0 + 8 * i, 1);
-      mbar_init(empty0 + 8 * i, 1);
+      for (int h = 0; h < C::kHalves; ++h) mbar_init(done0 + 8 * (h * C::kStages + i), 2);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(tfull0 + 8 * i, 1);
-      mbar_init(tempty0 + 8 * i, 4 * C::kGroups);
-    }
+    for (int i = 0; i < C::kHalves * C::kBufs; ++i) mbar_init(tempty0 + 8 * i, C::kWarps / C::kHalves * C::kPair);
     abort_flag = 0;
     fence_mbar_init();
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&tmem_slot), C::kTmemCols);
-    tmem_relinquish();
+    if (kPair) {
+      tmem_alloc_pair(smem_u32(&tmem_slot), C::kTmemCols);
+    } else {
+      tmem_alloc(smem_u32(&tmem_slot), C::kTmemCols);
+      tmem_relinquish();
+    }
   }
   tc_fence_before();
   __syncthreads();
+  if (kPair) cluster_sync_all();                       // the pair's barriers exist
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&tmem_slot);
   griddep_launch_dependents();
 
   // this CTA's tiles and its part of K
-  const int rank = p.split > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int k0 = static_cast<int>(static_cast<long long>(p.KB) * rank / p.split);
-  const int k1 = static_cast<int>(static_cast<long long>(p.KB) * (rank + 1) / p.split);
-  const int first = static_cast<int>(blockIdx.x) / p.split, step = static_cast<int>(gridDim.x) / p.split;
+  const int part = crank / C::kPair, per = p.split * C::kPair;
+  const int k0 = static_cast<int>(static_cast<long long>(p.KB) * part / p.split);
+  const int k1 = static_cast<int>(static_cast<long long>(p.KB) * (part + 1) / p.split);
+  const int first = static_cast<int>(blockIdx.x) / per, step = static_cast<int>(gridDim.x) / per;
   const int tiles = p.tiles_a * p.tiles_b;
+  const uint32_t freed0 = done0 + 8 * (C::kHalves - 1) * C::kStages;   // of a block's last MMA
   volatile int* const stop = &abort_flag;
+  auto give_up = [&] {
+    *stop = 1;
+    record_error(&g_fp8_status, kDevErrTimeout);
+  };
 
-  if (warp == 0 && lane == 0) {
-    // ---- producer.  The weight tiles of the first stages are requested before the wait
-    // for the kernel before this one, which may be writing the activation.
-    int pre = 0;
-    if (first < tiles) {
-      int ta, tb;
-      tile_at(first, p.tiles_a, p.tiles_b, ta, tb);
-      for (; pre < C::kStages && k0 + pre < k1; ++pre) {
-        const uint32_t st = smem + pre * C::kStageBytes;
-        mbar_arrive_expect_tx(full0 + 8 * pre, C::kStageBytes);
-        if (kSwap) tma_load_2d(st, &tm_a, full0 + 8 * pre, (k0 + pre) * kFp8Block, ta * 128);
-        else tma_load_2d(st + 16384, &tm_b, full0 + 8 * pre, (k0 + pre) * kFp8Block, tb * kBN);
-      }
-    }
-    griddep_wait();
-    int it = 0;
-    bool ok = true;
-    for (int t = first; ok && t < tiles; t += step) {
-      int ta, tb;
-      tile_at(t, p.tiles_a, p.tiles_b, ta, tb);
-      for (int kb = k0; kb < k1; ++kb, ++it) {
-        const int s = it % C::kStages;
-        const uint32_t st = smem + s * C::kStageBytes, bar = full0 + 8 * s;
-        const bool done = it < pre;          // its weight tile is on the way
-        if (it >= C::kStages && !mbar_wait(empty0 + 8 * s, (it / C::kStages + 1) & 1, stop)) {
-          ok = false;
-          break;
+  // Rows form: the promoting warps take registers from the others.
+  if (warp < 4) {
+    if (!kSwap) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegOther));
+    if (warp == 0) {
+      if (elect_one()) {
+        // ---- producer.  The weight tiles of the first stages are requested before the wait
+        // for the kernel before this one, which may be writing the activation.  A pair's
+        // loads are all counted on the first CTA's barrier.
+        auto load = [&](uint32_t dst, const CUtensorMap* m, int s, int kb, int row) {
+          if (kPair) tma_load_2d_pair(dst, m, mapa(full0 + 8 * s, crank & ~1), kb * kFp8Block, row);
+          else tma_load_2d(dst, m, full0 + 8 * s, kb * kFp8Block, row);
+        };
+        auto row_a = [&](int ta) { return kSwap ? ta * 128 : ta * 256 + half * 128; };
+        // rows form: 64 rows of either half of the tile's 256, the other CTA has the next 64
+        auto load_b = [&](uint32_t dst, int s, int kb, int tb) {
+          if (kSwap) {
+            load(dst, &tm_b, s, kb, tb * kBN);
+          } else {
+            load(dst, &tm_b, s, kb, tb * kBN + half * 64);
+            load(dst + 8192, &tm_b, s, kb, tb * kBN + 128 + half * 64);
+          }
+        };
+        int pre = 0;
+        if (first < tiles) {
+          int ta, tb;
+          tile_at(first, p.tiles_a, p.tiles_b, ta, tb);
+          for (; pre < C::kStages && k0 + pre < k1; ++pre) {
+            const uint32_t st = smem + pre * C::kStageBytes;
+            if (half == 0) mbar_arrive_expect_tx(full0 + 8 * pre, C::kStageBytes * C::kPair);
+            if (kSwap) load(st, &tm_a, pre, k0 + pre, row_a(ta));
+            else load_b(st + 16384, pre, k0 + pre, tb);
+          }
         }
-        if (!done) mbar_arrive_expect_tx(bar, C::kStageBytes);
-        if (!(kSwap && done)) tma_load_2d(st, &tm_a, bar, kb * kFp8Block, ta * 128);
-        if (kSwap || !done) tma_load_2d(st + 16384, &tm_b, bar, kb * kFp8Block, tb * kBN);
-      }
-    }
-    if (!ok) {
-      // give up: wait (bounded) for the copies in flight before the memory is left
-      *stop = 1;
-      record_error(&g_fp8_status, kDevErrTimeout);
-      const int zero = 0;
-      for (int j = max(0, it - C::kStages); j < it; ++j)
-        mbar_wait(full0 + 8 * (j % C::kStages), (j / C::kStages) & 1, &zero);
-    }
-  } else if (warp == 1 && lane == 0) {
-    // ---- MMA issuer
-    const uint32_t idesc = (1u << 4) | (static_cast<uint32_t>(kBN >> 3) << 17) | (8u << 24);
-    const SmemDesc a0 = make_sdesc(smem, 16, 1024, 2), b0 = make_sdesc(smem + 16384, 16, 1024, 2);
-    int it = 0;
-    bool ok = true;
-    for (int t = first; ok && t < tiles; t += step) {
-      for (int kb = k0; kb < k1; ++kb, ++it) {
-        const int s = it % C::kStages, buf = it & 1;
-        if ((it >= 2 && !mbar_wait(tempty0 + 8 * buf, (it / 2 + 1) & 1, stop)) ||
-            !mbar_wait(full0 + 8 * s, (it / C::kStages) & 1, stop)) {
-          ok = false;
-          break;
+        griddep_wait();
+        int it = 0, s = 0, phase = 1;
+        bool ok = true;
+        for (int t = first; ok && t < tiles; t += step) {
+          int ta, tb;
+          tile_at(t, p.tiles_a, p.tiles_b, ta, tb);
+          for (int kb = k0; kb < k1; ++kb, ++it) {
+            const uint32_t st = smem + s * C::kStageBytes;
+            const bool done = it < pre;          // its weight tile is on the way
+            if (it >= C::kStages && !mbar_wait(freed0 + 8 * s, phase, stop)) {
+              ok = false;
+              break;
+            }
+            if (!done && half == 0) mbar_arrive_expect_tx(full0 + 8 * s, C::kStageBytes * C::kPair);
+            if (!(kSwap && done)) load(st, &tm_a, s, kb, row_a(ta));
+            if (kSwap || !done) load_b(st + 16384, s, kb, tb);
+            if (++s == C::kStages) {
+              s = 0;
+              phase ^= 1;
+            }
+          }
         }
-        tc_fence_after();
-        const uint32_t off = static_cast<uint32_t>(s) * (C::kStageBytes >> 4);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          tc_mma_f8(tmem + buf * kBN, sdesc_at(a0, off + 2 * j), sdesc_at(b0, off + 2 * j), idesc, j > 0);
-        tc_commit(empty0 + 8 * s);
-        tc_commit(tfull0 + 8 * buf);
+        if (!ok) {
+          // give up: wait (bounded) for the copies in flight before the memory is left
+          give_up();
+          const int zero = 0;
+          if (half == 0)
+            for (int j = max(0, it - C::kStages); j < it; ++j)
+              mbar_wait(full0 + 8 * (j % C::kStages), (j / C::kStages) & 1, &zero);
+        }
       }
+    } else if (warp == 1) {
+      if (half == 0 && elect_one()) {
+        // ---- MMA issuer (the pair's first CTA)
+        const uint32_t idesc =
+            (1u << 4) | (static_cast<uint32_t>(C::kN >> 3) << 17) | (static_cast<uint32_t>(kPair ? 16 : 8) << 24);
+        const SmemDesc a0 = make_sdesc(smem, 16, 1024, 2), b0 = make_sdesc(smem + 16384, 16, 1024, 2);
+        int it = 0, s = 0, phase = 0, buf = 0, bphase = 1;
+        bool ok = true;
+        for (int t = first; ok && t < tiles; t += step) {
+          for (int kb = k0; kb < k1; ++kb, ++it) {
+            const uint32_t off = static_cast<uint32_t>(s) * (C::kStageBytes >> 4);
+  #pragma unroll
+            for (int h = 0; h < C::kHalves; ++h) {
+              if ((h == 0 && !mbar_wait(full0 + 8 * s, phase, stop)) ||
+                  (it >= C::kBufs && !mbar_wait(tempty0 + 8 * (h * C::kBufs + buf), bphase, stop))) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+  #pragma unroll
+              for (int j = 0; j < 4; ++j)
+                tc_mma_f8<kPair>(tmem + (h * C::kBufs + buf) * C::kN, sdesc_at(a0, off + 2 * j),
+                                 sdesc_at(b0, off + h * (8192 >> 4) + 2 * j), idesc, j > 0);
+              const uint32_t bar = done0 + 8 * (h * C::kStages + s);
+              if (kPair) tc_commit_pair(bar, static_cast<uint16_t>(3u << (crank & ~1)));
+              else tc_commit(bar);
+            }
+            if (!ok) break;
+            if (++s == C::kStages) {
+              s = 0;
+              phase ^= 1;
+            }
+            if (++buf == C::kBufs) {
+              buf = 0;
+              bphase ^= 1;
+            }
+          }
+        }
+        if (!ok) {
+          give_up();
+          // the products issued last end before the tensor memory is freed (bounded)
+          const int zero = 0;
+          for (int j = max(0, it - C::kBufs); j < it; ++j)
+            mbar_wait(done0 + 8 * ((C::kHalves - 1) * C::kStages + j % C::kStages), (j / C::kStages) & 1, &zero);
+        }
+      }
+    } else if (warp == 2) {
+      // ---- scales: one ring slot per block, four blocks' loads in flight.  Swapped form:
+      // each token's scale times the tile's weight scale; rows form: this CTA's 128 tokens'
+      // scales, then the two weight scales of the tile's columns.  A block's "done" barriers
+      // wait for its scales as well as for its MMAs, so block b may be filled in once block
+      // b - kStages is done.  Its slot is then free too: the slot's last block, b - kStages -
+      // kBufs, was read before the MMAs of block b - kStages were issued.
+      griddep_wait();
+      constexpr int kPer = (C::kTok + 31) / 32;
+      int it = 0;
+      bool ok = true;
+      for (int t = first; ok && t < tiles; t += step) {
+        int ta, tb;
+        tile_at(t, p.tiles_a, p.tiles_b, ta, tb);
+        const int tok0 = kSwap ? 0 : ta * 256 + half * 128;
+        const int wblk = kSwap ? ta : tb * 2 + (lane & 1);
+        const float* pw = p.ws + static_cast<long long>(min(wblk, p.NB - 1)) * p.KB;
+        for (int kb = k0; ok && kb < k1; kb += 4) {
+          float s[4][kPer], w[4];
+  #pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const bool in = kb + q < k1;
+            w[q] = in ? __ldg(pw + kb + q) : 0.0f;
+  #pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+              const int m = tok0 + j * 32 + lane;
+              const bool has = in && j * 32 + lane < C::kTok && m < p.M;
+              s[q][j] = has ? __ldg(p.xs + static_cast<long long>(kb + q) * p.M + m) : 0.0f;
+            }
+          }
+  #pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (!ok || kb + q >= k1) break;
+            const int slot = it % C::kRing, prev = it - C::kStages;
+            const bool late =
+                prev >= 0 && !mbar_wait(freed0 + 8 * (prev % C::kStages), (prev / C::kStages) & 1, stop);
+            if (__any_sync(0xFFFFFFFFu, late)) {
+              ok = false;
+              break;
+            }
+  #pragma unroll
+            for (int j = 0; j < kPer; ++j)
+              if (j * 32 + lane < C::kTok) ring[slot][j * 32 + lane] = kSwap ? s[q][j] * w[q] : s[q][j];
+            if (!kSwap && lane < 2) ring[slot][C::kTok + lane] = w[q];
+            __syncwarp();
+            if (lane < C::kHalves) mbar_arrive(done0 + 8 * (lane * C::kStages + it % C::kStages));
+            ++it;
+          }
+        }
+      }
+      if (!ok) give_up();
     }
-    if (!ok) {
-      *stop = 1;
-      record_error(&g_fp8_status, kDevErrTimeout);
-      // the products issued last end before the tensor memory is freed (bounded)
-      const int zero = 0;
-      for (int j = max(0, it - 2); j < it; ++j) mbar_wait(tfull0 + 8 * (j & 1), (j / 2) & 1, &zero);
-    }
-  } else if (warp >= 4) {
+    __syncwarp();
+    if (!kSwap) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegLaunch));
+  } else {
     // ---- promotion: one thread per MMA row and group of kCols columns
+    if (!kSwap) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegPromote));
     griddep_wait();
     const int grp = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
-    const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + grp * C::kCols;
-    int it = 0;
+    const int sub = kSwap ? 0 : grp >> 1;                     // rows form: this group's half of the tile
+    const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) +
+                           (kSwap ? grp * C::kCols : sub * C::kBufs * C::kN + (grp & 1) * C::kCols);
+    const uint32_t free0 = tempty0 + 8 * sub * C::kBufs, done_g = done0 + 8 * sub * C::kStages;
+    const uint32_t release0 = kPair ? mapa(free0, crank & ~1) : free0;
+    int s = 0, phase = 0, buf = 0, slot = 0;
     bool ok = true;
+    // the next block's sums and scales are ready (all lanes of the warp agree)
+    auto wait_block = [&] {
+      if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(done_g + 8 * s, phase)) &&
+          __any_sync(0xFFFFFFFFu, !mbar_wait_slow(done_g + 8 * s, phase, stop))) {
+        ok = false;
+        give_up();
+      }
+      tc_fence_after();
+      return ok;
+    };
+    auto release = [&] {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (kPair) mbar_arrive_cluster(release0 + 8 * buf);
+        else mbar_arrive(release0 + 8 * buf);
+      }
+    };
+    auto advance = [&] {
+      if (++s == C::kStages) {
+        s = 0;
+        phase ^= 1;
+      }
+      if (++buf == C::kBufs) buf = 0;
+      if (++slot == C::kRing) slot = 0;
+    };
     for (int t = first; ok && t < tiles; t += step) {
       int ta, tb;
       tile_at(t, p.tiles_a, p.tiles_b, ta, tb);
       uint64_t acc[C::kCols / 2];
 #pragma unroll
       for (int j = 0; j < C::kCols / 2; ++j) acc[j] = 0;
-      // rows form: this row's token and these columns' weight block; swapped form:
-      // thread j < kBN holds the scale of column (token) j, and the tile's weight block
-      const int wblk = kSwap ? ta : tb * (kBN / 128) + grp;
-      const int tok = kSwap ? tb * kBN + row : ta * 128 + row;
-      const bool has = tok < p.M && (!kSwap || row < kBN) && wblk < p.NB;
-      const float* ps = p.xs + (has ? tok : 0);
-      const float* pw = p.ws + static_cast<long long>(has ? wblk : 0) * p.KB;
-      auto scale_of = [&](int kb) {
-        return has ? __ldg(ps + static_cast<long long>(kb) * p.M) * __ldg(pw + kb) : 0.0f;
-      };
-      float s_next = k0 < k1 ? scale_of(k0) : 0.0f;
-      for (int kb = k0; kb < k1; ++kb, ++it) {
-        const float s = s_next;
-        if (kb + 1 < k1) s_next = scale_of(kb + 1);
-        const int buf = it & 1;
-        if (kSwap) {
-          if (row < kBN) col_scale[buf][row] = s;
-          named_barrier(1, 128);
-        }
-        if (!mbar_wait(tfull0 + 8 * buf, (it / 2) & 1, stop)) {
-          ok = false;
-          // the other threads of the group reach their own wait and see the flag
-          *stop = 1;
-          record_error(&g_fp8_status, kDevErrTimeout);
-        }
-        if (kSwap ? named_barrier_or(2, 128, !ok) : __any_sync(0xFFFFFFFFu, !ok)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t src = taddr + buf * kBN;
-        const uint64_t s2 = f32x2_pack(__float_as_uint(s), __float_as_uint(s));
+      if constexpr (kSwap) {
+        for (int kb = k0; kb < k1; ++kb) {
+          if (!wait_block()) break;
+          // the scales are read before the accumulator (and with it their slot) is released
+          const float* cs = &ring[slot][grp * C::kCols];
+          const uint32_t src = taddr + buf * C::kN;
 #pragma unroll
-        for (int c = 0; c < C::kCols; c += 16) {
-          uint32_t d[16];
-          tmem_ld16(src + c, d);
+          for (int c = 0; c < C::kCols; c += 16) {
+            uint64_t f[8];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint64_t f = s2;
-            if (kSwap) f = *reinterpret_cast<const uint64_t*>(&col_scale[buf][(c + 2 * j) % (kSwap ? kBN : 4)]);
-            acc[c / 2 + j] = f32x2_fma(f32x2_pack(d[2 * j], d[2 * j + 1]), f, acc[c / 2 + j]);
+            for (int j = 0; j < 8; j += 2) {
+              const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(cs + c + 2 * j);
+              f[j] = q.x;
+              f[j + 1] = q.y;
+            }
+            uint32_t d[16];
+            tmem_ld16(src + c, d);
+            if (c + 16 == C::kCols) release();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              acc[c / 2 + j] = f32x2_fma(f32x2_pack(d[2 * j], d[2 * j + 1]), f[j], acc[c / 2 + j]);
           }
+          advance();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(tempty0 + 8 * buf);
+      } else {
+        for (int kb = k0; kb < k1; ++kb) {
+          if (!wait_block()) break;
+          const uint32_t src = taddr + buf * C::kN;
+          const float v = ring[slot][row] * ring[slot][C::kTok + sub];
+          const uint64_t f = f32x2_pack(__float_as_uint(v), __float_as_uint(v));
+#pragma unroll
+          for (int c = 0; c < C::kCols; c += 16) {
+            uint32_t d[16];
+            tmem_ld16(src + c, d);
+            if (c + 16 == C::kCols) release();
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              acc[c / 2 + j] = f32x2_fma(f32x2_pack(d[2 * j], d[2 * j + 1]), f, acc[c / 2 + j]);
+          }
+          advance();
+        }
       }
       float v[C::kCols];
 #pragma unroll
       for (int j = 0; j < C::kCols / 2; ++j)
         asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2 * j]), "=f"(v[2 * j + 1]) : "l"(acc[j]));
       if (p.split > 1) {
-        // every product of this CTA is done: its stages are free for the exchange
+        // every product of this CTA's part is done: the stages are free for the exchange
         float* x = reinterpret_cast<float*>(smem_raw + (smem - smem_u32(smem_raw)));
         if (kSwap) {
 #pragma unroll
-          for (int j = 0; j < C::kCols; ++j) x[j * C::kPitch + row] = v[j];
+          for (int j = 0; j < C::kCols; ++j) x[(grp * C::kCols + j) * C::kPitch + row] = v[j];
         } else {
 #pragma unroll
           for (int j = 0; j < C::kCols; j += 4)
@@ -353,59 +569,116 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
           if (n < p.N) {
 #pragma unroll
             for (int j = 0; j < C::kCols; ++j)
-              if (tb * kBN + j < p.M) store_one(p, static_cast<long long>(tb * kBN + j) * p.N + n, v[j]);
+              if (grp * C::kCols + j < p.M) store_one(p, static_cast<long long>(grp * C::kCols + j) * p.N + n, v[j]);
           }
         } else {
-          const int n = tb * kBN + grp * C::kCols;
+          const int tok = ta * 256 + half * 128 + row, n = tb * kBN + grp * C::kCols;
           if (tok < p.M && n < p.N) store_row<C::kCols>(p, static_cast<long long>(tok) * p.N + n, p.N - n, v);
         }
       }
     }
+    __syncwarp();
+    if (!kSwap) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegLaunch));
   }
 
   // every role comes here, in the failing case too
   __syncthreads();
   if (p.split > 1) {
     cluster_sync_all();
-    // output rows of the exchange: tokens; this CTA finishes rows rank, rank + split, ...
+    // output rows of the exchange: tokens; this CTA finishes rows part, part + split, ...
     int ta, tb;
     tile_at(first, p.tiles_a, p.tiles_b, ta, tb);
-    const int m0 = kSwap ? tb * kBN : ta * 128, n0 = kSwap ? ta * 128 : tb * kBN;
+    const int m0 = kSwap ? tb * kBN : ta * 256 + half * 128, n0 = kSwap ? ta * 128 : tb * kBN;
     constexpr int kRows = kSwap ? kBN : 128, kWide = kSwap ? 128 : kBN;
-    const int rows = min(kRows, p.M - m0);
+    const int rows = max(0, min(kRows, p.M - m0) - part);
     const bool good = *stop == 0;
-    for (int i = tid; i < kWide * ((rows - rank + p.split - 1) / p.split); i += C::kThreads) {
-      const int c = i % kWide, r = rank + i / kWide * p.split;
-      float sum = 0.0f;
-      for (int q = 0; q < p.split; ++q) sum += ld_dsmem(mapa(smem + (r * C::kPitch + c) * 4, q));
-      if (good && n0 + c < p.N) store_one(p, static_cast<long long>(m0 + r) * p.N + n0 + c, sum);
+    for (int i = tid; i < kWide / 4 * ((rows + p.split - 1) / p.split); i += C::kThreads) {
+      const int c = i % (kWide / 4) * 4, r = part + i / (kWide / 4) * p.split;
+      const uint32_t at = smem + (r * C::kPitch + c) * 4;
+      float4 v[8 / C::kPair];                          // all parts' loads in flight, added in rank order
+#pragma unroll
+      for (int q = 0; q < 8 / C::kPair; ++q)
+        v[q] = q < p.split ? ld_dsmem4(mapa(at, q * C::kPair + half)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      float sum[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
+#pragma unroll
+      for (int q = 1; q < 8 / C::kPair; ++q) {
+        if (q >= p.split) break;
+        sum[0] += v[q].x;
+        sum[1] += v[q].y;
+        sum[2] += v[q].z;
+        sum[3] += v[q].w;
+      }
+      if (good && n0 + c < p.N) store4(p, static_cast<long long>(m0 + r) * p.N + n0 + c, p.N - n0 - c, sum);
     }
-    cluster_sync_all();
   }
+  // nothing of a CTA that another one of the cluster reads or writes goes away early
+  if (kPair || p.split > 1) cluster_sync_all();
   __syncwarp();
-  if (warp == 1) tmem_dealloc(tmem, C::kTmemCols);
+  if (warp == 1) {
+    if (kPair) tmem_dealloc_pair(tmem, C::kTmemCols);
+    else tmem_dealloc(tmem, C::kTmemCols);
+  }
 }
+
+// What an instance needs to know about a device, found out on first use.
+struct DeviceSetup {
+  std::once_flag once;
+  cudaError_t err = cudaSuccess;
+  int clusters[9] = {};        // clusters of 1..8 parts (pairs in the rows form) resident at once
+};
+constexpr int kMaxDevices = 64;
 
 template <bool kSwap, int kBN>
 cudaError_t launch_instance(const CUtensorMap& ta, const CUtensorMap& tb, Fp8GemmParams& p, cudaStream_t s) {
   using C = Cfg<kSwap, kBN>;
-  static std::atomic<unsigned long long> ready{0};       // devices whose shared-memory limit is raised
+  constexpr int kMaxSplit = 8 / C::kPair;
+  static DeviceSetup setups[kMaxDevices];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (!(ready.load() & bit)) {
-    e = cudaFuncSetAttribute(fp8_gemm_kernel<kSwap, kBN>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
-    if (e != cudaSuccess) return e;
-    ready.fetch_or(bit);
-  }
+  if (dev >= kMaxDevices) return cudaErrorInvalidDevice;
+  DeviceSetup& d = setups[dev];
+  auto kernel = fp8_gemm_kernel<kSwap, kBN>;
+  std::call_once(d.once, [&] {
+    d.err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (d.err != cudaSuccess) return;
+    cudaFuncAttributes fa;
+    d.err = cudaFuncGetAttributes(&fa, kernel);
+    if (d.err != cudaSuccess) return;
+    // setmaxnreg hands out the registers that the block was launched with; with fewer of
+    // them the promoting warps would wait for ever
+    if (!kSwap && fa.numRegs * C::kThreads < C::kRegTotal) {
+      d.err = cudaErrorInvalidKernelImage;
+      return;
+    }
+    for (int split = 1; split <= kMaxSplit; ++split) {
+      cudaLaunchConfig_t cfg = {};
+      cfg.gridDim = dim3(static_cast<unsigned>(split * C::kPair));
+      cfg.blockDim = dim3(C::kThreads);
+      cfg.dynamicSmemBytes = C::kSmem;
+      cudaLaunchAttribute attr;
+      attr.id = cudaLaunchAttributeClusterDimension;
+      attr.val.clusterDim.x = static_cast<unsigned>(split * C::kPair);
+      attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+      cfg.attrs = &attr;
+      cfg.numAttrs = 1;
+      d.err = cudaOccupancyMaxActiveClusters(&d.clusters[split], kernel, &cfg);
+      if (d.err != cudaSuccess) return;
+    }
+  });
+  if (d.err != cudaSuccess) return d.err;
+  // K is split as far as all clusters still run at once: the weight's stream (or a tile's
+  // chain of blocks) gets shorter with every part, a second wave costs more than it saves.
+  // Measured, us at M, N, K (parts): 1, 5120, 5120: 13.3 (1), 8.1 (4), 7.7 (5), 12.7 (7, which
+  // does not fit); 129, 5120, 5120: 24.2 (1), 16.3 (3), 27.1 (4, does not fit).
   const long long tiles = static_cast<long long>(p.tiles_a) * p.tiles_b;
-  const int slots = num_sms() * C::kCtasPerSm;
   int split = 1;
-  while (split < 8 && split < p.KB && tiles * (split + 1) <= slots) ++split;
+  for (int q = 2; q <= kMaxSplit && q <= p.KB; ++q)
+    if (tiles <= d.clusters[q]) split = q;
   p.split = split;
-  const unsigned grid = static_cast<unsigned>(split > 1 ? tiles * split : tiles < slots ? tiles : slots);
-  return launch_pdl(fp8_gemm_kernel<kSwap, kBN>, grid, C::kThreads, C::kSmem, split, s, ta, tb, p);
+  const long long slots = d.clusters[1];
+  const unsigned groups = static_cast<unsigned>(split > 1 ? tiles * split : tiles < slots ? tiles : slots);
+  return launch_pdl(kernel, groups * C::kPair, C::kThreads, C::kSmem, split * C::kPair, s, ta, tb, p);
 }
 
 }  // namespace
@@ -437,14 +710,14 @@ int run_fp8_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const fl
   p.NB = (N + 127) / 128;
   p.y_f32 = y_f32;
   const unsigned long long bits = reinterpret_cast<uintptr_t>(y) | static_cast<unsigned long long>(N) * (y_f32 ? 4 : 2);
-  p.vec = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : 2;
+  p.vec = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : 2;
   const bool swap = M <= 128;
   const int bn = !swap ? 256 : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-  p.tiles_a = swap ? p.NB : (M + 127) / 128;
+  p.tiles_a = swap ? p.NB : (M + 255) / 256;
   p.tiles_b = swap ? 1 : (N + bn - 1) / bn;
   if (static_cast<long long>(p.tiles_a) * p.tiles_b > 0x7FFFFFFFLL) return BILOCO_ERR_SHAPE;
   CUtensorMap tx, tw;
-  if (!make_tmap(&tx, xq, K, M, swap ? bn : 128) || !make_tmap(&tw, wq, K, N, swap ? 128 : bn)) return BILOCO_ERR_CUDA;
+  if (!make_tmap(&tx, xq, K, M, swap ? bn : 128) || !make_tmap(&tw, wq, K, N, swap ? 128 : 64)) return BILOCO_ERR_CUDA;
   cudaError_t e;
   if (!swap) e = launch_instance<false, 256>(tx, tw, p, s);
   else if (bn == 16) e = launch_instance<true, 16>(tw, tx, p, s);
