@@ -343,6 +343,47 @@ int biloco_block_norm(const void *y_bf16, long long ldy, const void *h, long lon
                       void *x_bf16, uint8_t *codes, float *scales, biloco_stream_t stream);
 
 /*
+ * biloco_fp8_moe - a whole mixture-of-experts layer for a few tokens (up to 64).
+ *     score of expert e for token t: softmax over the experts, or sigmoid, of x[t] . router[e]
+ *     its k experts: the largest scores (with bias: of score + bias), ties to the lowest index
+ *     weight: the score itself (renorm: divided by the sum over the k), times route_scale
+ *     y[t] = sum over its experts of weight * W2_e (silu(W1_e x[t]) * (W3_e x[t]))
+ *   x_bf16   [T][D] bfloat16, row stride ldx (multiple of 8), not quantised
+ *   router   [E][D] of router_type; bias [E] float, for the choice only, or NULL
+ *   w13      [E + shared][2F][D] codes and their scales (biloco_fp8_pack_weight on E + shared
+ *            weights [2F][D]): rows 0..F-1 are W1 (gate), F..2F-1 are W3 (up)
+ *   w2       [E + shared][D][F] codes and scales
+ *   shared   the last `shared` experts serve every token with weight 1
+ *   y_bf16   out [T][D]; ids out [T][k] int, weights out [T][k] float, in the order picked
+ *   workspace  device memory of at least biloco_fp8_moe_workspace_bytes (256-byte aligned),
+ *            owned by the caller; its contents do not matter before the call and are of no
+ *            use after it.  Two calls that may overlap need two of them.
+ *   limits   0 <= T <= 64 (0: nothing is done), D and F multiples of 16 up to 16384,
+ *            1 <= k <= 16, k <= E <= 512, 0 <= shared <= 4
+ * Scores are summed to better than FP32 and compared in FP64; a score that is not a number
+ * is picked last.  The products are FP16 x E4M3 with FP32 sums: rows of x are scaled into
+ * FP16 exactly (BF16 values more than 2^29 below the row's largest lose bits), the hidden
+ * values are rounded to FP16.  A token with an infinity or NaN spoils only its own row.
+ * Three kernels with programmatic dependent launch; w2 may be read before the kernel before
+ * them on the stream has ended (see biloco_gemm on what must not write the weight).
+ * The result depends only on the operands and the shape.
+ */
+#define BILOCO_MOE_MAX_T 64
+#define BILOCO_MOE_MAX_D 16384
+#define BILOCO_MOE_MAX_F 16384
+#define BILOCO_MOE_MAX_E 512
+#define BILOCO_MOE_MAX_K 16
+#define BILOCO_MOE_MAX_SHARED 4
+enum { BILOCO_SCORE_SOFTMAX = 0, BILOCO_SCORE_SIGMOID = 1 };
+size_t biloco_fp8_moe_workspace_bytes(int T, int D, int F, int k, int shared);
+int biloco_fp8_moe(const void *x_bf16, long long ldx, const void *router, int router_type,
+                   const float *bias, const uint8_t *w13_codes, const float *w13_scales,
+                   const uint8_t *w2_codes, const float *w2_scales, int T, int D, int F, int E,
+                   int k, int shared, int score, int renorm, float route_scale, void *y_bf16,
+                   int *ids, float *weights, void *workspace, size_t workspace_bytes,
+                   biloco_stream_t stream);
+
+/*
  * Launch form of the GEMM kernels for later biloco_gemm / biloco_gemm_noalloc
  * calls (process-wide), a combination of:
  *   BILOCO_LAUNCH_PDL          programmatic dependent launch: the kernel may start

@@ -14,4 +14,4 @@ from ._lib import (  # noqa: F401
     last_error, load, pack_signs, pack_weight, quant_act, resolve_mode, set_mode, shutdown,
     status_string, weight_sf_bytes,
 )
-from ._fp8 import block_norm, fp8_gemm, fp8_pack_weight, fp8_quant_act  # noqa: F401
+from ._fp8 import block_norm, fp8_gemm, fp8_moe, fp8_pack_weight, fp8_quant_act  # noqa: F401

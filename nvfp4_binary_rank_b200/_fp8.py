@@ -198,3 +198,56 @@ def block_norm(y: torch.Tensor | None, h: torch.Tensor | None, *, post_weight: t
     if quant:
         return out_h, codes, scales
     return out_h if x is None else (out_h, x)
+
+
+_SCORE = {"softmax": 0, "sigmoid": 1}
+
+
+def fp8_moe(x: torch.Tensor, router: torch.Tensor, w13: torch.Tensor, w13_scales: torch.Tensor, w2: torch.Tensor,
+            w2_scales: torch.Tensor, top_k: int, *, score: str = "softmax", bias: torch.Tensor | None = None,
+            renorm: bool = True, route_scale: float = 1.0, stream=None):
+    """A whole mixture-of-experts layer for up to 64 tokens:
+
+        y[t] = sum over t's top_k experts e of weight[t, e] W2_e (silu(W1_e x[t]) * (W3_e x[t]))
+
+    x bfloat16 [T, D]; router bfloat16 or float32 [E, D]; w13 [n, 2F, D] ([W1; W3] stacked)
+    and w2 [n, D, F] with their scales from fp8_pack_weight.  The n - E last experts are
+    shared: they serve every token with weight 1.  `score` is "softmax" (over the experts)
+    or "sigmoid"; bias float32 [E] is added for the choice only.  Returns (y bfloat16
+    [T, D], ids int32 [T, top_k], weights float32 [T, top_k])."""
+    _tensor(x, "x", (_BF16,), 2)
+    _tensor(router, "router", (_BF16, _F32), 2)
+    _tensor(w13, "w13", (_FP8,), 3)
+    T, D = x.shape
+    E, n, F = router.shape[0], w13.shape[0], w13.shape[1] // 2
+    dev = x.device
+    ld = _rows(x, "x")
+    KD, KF = (D + 127) // 128, (F + 127) // 128
+    _dense(router, "router", (_BF16, _F32), (E, D), dev)
+    _dense(w13, "w13", (_FP8,), (n, 2 * F, D), dev)
+    _dense(w13_scales, "w13_scales", (_F32,), (n, (2 * F + 127) // 128, KD), dev)
+    _dense(w2, "w2", (_FP8,), (n, D, F), dev)
+    _dense(w2_scales, "w2_scales", (_F32,), (n, KD, KF), dev)
+    if n < E:
+        raise ValueError(f"router has {E} experts, w13 {n}")
+    if bias is not None:
+        _dense(bias, "bias", (_F32,), (E,), dev)
+    if not 1 <= top_k <= E:
+        raise ValueError(f"top_k must be 1 to {E}, got {top_k}")
+    if score not in _SCORE:
+        raise ValueError(f"score must be one of {sorted(_SCORE)}, got {score!r}")
+    lib = _lib.load()
+    with _on(dev, stream):
+        y = torch.empty((T, D), dtype=_BF16, device=dev)
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        weights = torch.empty((T, top_k), dtype=_F32, device=dev)
+        nbytes = lib.biloco_fp8_moe_workspace_bytes(T, D, F, top_k, n - E) if T else 1
+        if nbytes == 0:
+            raise _lib.BilocoError("biloco_fp8_moe_workspace_bytes", _lib.ERR_SHAPE)
+        ws = torch.empty((nbytes,), dtype=torch.uint8, device=dev)
+        _check("biloco_fp8_moe", lib.biloco_fp8_moe(
+            x.data_ptr(), ld, router.data_ptr(), _TYPE[router.dtype], None if bias is None else bias.data_ptr(),
+            w13.data_ptr(), w13_scales.data_ptr(), w2.data_ptr(), w2_scales.data_ptr(), T, D, F, E, top_k, n - E,
+            _SCORE[score], int(renorm), route_scale, y.data_ptr(), ids.data_ptr(), weights.data_ptr(), ws.data_ptr(),
+            nbytes, _raw_stream(dev.index)))
+    return y, ids, weights

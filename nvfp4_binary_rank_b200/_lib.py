@@ -46,6 +46,9 @@ SIGNATURES = {
     "biloco_fp8_pack_weight": (_I, [_P, _I, _I, _I, _I, _P, _P, _P]),
     "biloco_fp8_gemm": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
     "biloco_block_norm": (_I, [_P, _L, _P, _L, _I, _P, _P, _I, _P, _I, _I, _F, _F, _F, _I, _I, _P, _L, _P, _P, _P, _P]),
+    "biloco_fp8_moe_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
+    "biloco_fp8_moe": (_I, [_P, _L, _P, _I, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _F, _P, _P, _P, _P,
+                            ctypes.c_size_t, _P]),
     "biloco_set_mode": (_I, [_I]),
     "biloco_resolve_mode": (_I, [_I, _I, _I, _I]),
     "biloco_last_error": (_I, [_P]),

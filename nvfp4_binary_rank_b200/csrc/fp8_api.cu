@@ -5,6 +5,7 @@
 
 #include "../../include/biloco.h"
 #include "fp8_dev.cuh"
+#include "fp8_moe.h"
 #include "fp8_ops.h"
 #include "internal.h"
 
@@ -101,6 +102,64 @@ int biloco_block_norm(const void* y_bf16, long long ldy, const void* h, long lon
   a.w_f32 = w_type == BILOCO_TYPE_F32;
   a.gate_f32 = gate_type == BILOCO_TYPE_F32;
   return status_of(launch_block_norm(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t biloco_fp8_moe_workspace_bytes(int T, int D, int F, int k, int shared) {
+  if (T < 1 || T > BILOCO_MOE_MAX_T || D < 16 || D % 16 || D > BILOCO_MOE_MAX_D || F < 16 || F % 16 ||
+      F > BILOCO_MOE_MAX_F || k < 1 || k > BILOCO_MOE_MAX_K || shared < 0 || shared > BILOCO_MOE_MAX_SHARED)
+    return 0;
+  MoeArgs a = {};
+  a.T = T;
+  a.D = D;
+  a.F = F;
+  a.k = k;
+  a.shared = shared;
+  return moe_carve(a, nullptr);
+}
+
+int biloco_fp8_moe(const void* x_bf16, long long ldx, const void* router, int router_type, const float* bias,
+                   const uint8_t* w13_codes, const float* w13_scales, const uint8_t* w2_codes, const float* w2_scales,
+                   int T, int D, int F, int E, int k, int shared, int score, int renorm, float route_scale,
+                   void* y_bf16, int* ids, float* weights, void* workspace, size_t workspace_bytes,
+                   biloco_stream_t stream) {
+  if (T < 0 || bad_type(router_type) || (score != BILOCO_SCORE_SOFTMAX && score != BILOCO_SCORE_SIGMOID))
+    return BILOCO_ERR_ARG;
+  if (T == 0) return BILOCO_OK;
+  if (!x_bf16 || !router || !w13_codes || !w13_scales || !w2_codes || !w2_scales || !y_bf16 || !ids || !weights ||
+      !workspace)
+    return BILOCO_ERR_ARG;
+  const size_t need = biloco_fp8_moe_workspace_bytes(T, D, F, k, shared);
+  if (!need || E < 1 || E > BILOCO_MOE_MAX_E || k > E || ldx < D || ldx % 8) return BILOCO_ERR_SHAPE;
+  if (workspace_bytes < need) return BILOCO_ERR_ARG;
+  if (off(x_bf16, 16) || off(router, 16) || off(bias, 4) || off(w13_codes, 16) || off(w13_scales, 4) ||
+      off(w2_codes, 16) || off(w2_scales, 4) || off(y_bf16, 2) || off(ids, 4) || off(weights, 4) || off(workspace, 256))
+    return BILOCO_ERR_ALIGN;
+  const int d = check_device();
+  if (d) return d;
+  MoeArgs a = {};
+  a.x = static_cast<const uint16_t*>(x_bf16);
+  a.router = router;
+  a.bias = bias;
+  a.w13 = w13_codes;
+  a.s13 = w13_scales;
+  a.w2 = w2_codes;
+  a.s2 = w2_scales;
+  a.y = static_cast<uint16_t*>(y_bf16);
+  a.ids = ids;
+  a.weights = weights;
+  a.ldx = ldx;
+  a.T = T;
+  a.D = D;
+  a.F = F;
+  a.E = E;
+  a.k = k;
+  a.shared = shared;
+  a.sigmoid = score == BILOCO_SCORE_SIGMOID;
+  a.renorm = renorm != 0;
+  a.router_f32 = router_type == BILOCO_TYPE_F32;
+  a.route_scale = route_scale;
+  moe_carve(a, static_cast<uint8_t*>(workspace));
+  return status_of(launch_fp8_moe(a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -152,6 +152,36 @@ def test_block_norm_refusals(lib):
     assert _norm(lib, post=P(0x10008)) == -3
 
 
+def _moe(lib, x=A, ldx=64, router=A, rt=0, w13=A, T=2, D=64, F=32, E=4, k=2, sh=0, score=0, y=A, ws=A, nbytes=1 << 30):
+    return lib.biloco_fp8_moe(x, ldx, router, rt, None, w13, A, A, A, T, D, F, E, k, sh, score, 1, 1.0, y, A, A, ws,
+                              nbytes, None)
+
+
+def test_fp8_moe_refusals(lib):
+    assert _moe(lib, x=None) == -1
+    assert _moe(lib, ws=None) == -1
+    assert _moe(lib, rt=5) == -1
+    assert _moe(lib, score=2) == -1
+    assert _moe(lib, T=-1) == -1
+    assert _moe(lib, nbytes=64) == -1
+    assert _moe(lib, T=65) == -2
+    assert _moe(lib, D=72, ldx=72) == -2
+    assert _moe(lib, F=24) == -2
+    assert _moe(lib, F=16400) == -2
+    assert _moe(lib, k=5) == -2
+    assert _moe(lib, k=0) == -2
+    assert _moe(lib, E=513) == -2
+    assert _moe(lib, k=17, E=32) == -2
+    assert _moe(lib, sh=5) == -2
+    assert _moe(lib, ldx=48) == -2
+    assert _moe(lib, x=P(0x10008)) == -3
+    assert _moe(lib, w13=P(0x10008)) == -3
+    assert _moe(lib, ws=P(0x10010)) == -3
+    assert _moe(lib, T=0, x=None, ws=None) == 0
+    assert lib.biloco_fp8_moe_workspace_bytes(1, 64, 32, 2, 0) > 0
+    assert lib.biloco_fp8_moe_workspace_bytes(0, 64, 32, 2, 0) == 0
+
+
 def test_binding_refuses_host_tensors():
     import nvfp4_binary_rank_b200 as nb
     x = torch.zeros((2, 64), dtype=torch.bfloat16)
