@@ -102,174 +102,177 @@ __device__ __forceinline__ void load_router8(const void* p, long long at, float 
   }
 }
 
+// Order-preserving integer key of a score: larger is better, 0 stands for "taken".  A score
+// that is no number gets 1, below every number.
+__device__ __forceinline__ unsigned long long order_key(double v) {
+  const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(v));
+  if (isnan(v)) return 1;
+  return (b >> 63) ? ~b + 1 : b | 0x8000000000000001ull;
+}
+
 // A cluster of eight CTAs serves kTok tokens: each CTA scores an eighth of the experts for
-// all of them (the router is read once per cluster), the first one picks.
+// all of them (the router is read once per cluster), the first one picks.  Loops are kept
+// rolled: one launch of a few CTAs pays for every instruction line it fetches (with the
+// selection unrolled over 512 experts the kernel took 18 us, mostly instruction misses).
 template <int kTok, bool kF32>
 __global__ void __launch_bounds__(kThreads)
 moe_route_kernel(const __grid_constant__ MoeArgs a) {
-  extern __shared__ __align__(16) uint8_t sm[];
-  uint16_t* xs = reinterpret_cast<uint16_t*>(sm);                       // [kTok][D] bf16
-  __shared__ double logits[kTok][kMoeMaxExperts];
+  __shared__ double score[kTok][kMoeMaxExperts];                        // the scores, then the weights
+  __shared__ unsigned long long key[kTok][kMoeMaxExperts];
   __shared__ uint32_t part[kTok][kWarps];
   griddep_launch_dependents();
   griddep_wait();
+  // the first CTA's shared memory may be written once that CTA runs
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(cta_rank());
   const int t0 = static_cast<int>(blockIdx.x) / kRouteCtas * kTok;
-  const int D = a.D, nvec = D / 8;
-
-  // the token rows into shared memory, and each row's largest magnitude
-  uint32_t top[kTok];
-#pragma unroll
-  for (int j = 0; j < kTok; ++j) {
-    top[j] = 0;
-    if (t0 + j < a.T) {
-      for (int c = tid; c < nvec; c += kThreads) {
-        const uint4 q = __ldg(reinterpret_cast<const uint4*>(a.x + (t0 + j) * a.ldx) + c);
-        reinterpret_cast<uint4*>(xs + j * D)[c] = q;
-        const uint32_t m = __vmaxu2(__vmaxu2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu),
-                                    __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu));
-        top[j] = max(top[j], max(m << 16, m & 0xFFFF0000u));
-      }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) top[j] = max(top[j], __shfl_xor_sync(0xFFFFFFFFu, top[j], o));
-    if (lane == 0) part[j][warp] = top[j];
-  }
-  cluster_barrier();                // also: the first CTA runs, so its shared memory may be written
+  const int D = a.D, nvec = D / 8, ntok = min(kTok, a.T - t0);
+  const uint16_t* x = a.x + t0 * a.ldx;
+  bool joined = false;
 
   // scores: a warp takes whole experts; sums of eight products, compensated over a lane's
   // eights (Kahan), in FP64 over the lanes
-  const uint32_t remote = mapa_u32(smem_u32(&logits[0][0]), 0);
+  const uint32_t remote = mapa_u32(smem_u32(&score[0][0]), 0);
+#pragma unroll 1
   for (int e = rank + kRouteCtas * warp; e < a.E; e += kRouteCtas * kWarps) {
     float s[kTok], comp[kTok];
 #pragma unroll
     for (int j = 0; j < kTok; ++j) s[j] = comp[j] = 0.0f;
-#pragma unroll 2
+#pragma unroll 4
     for (int c = lane; c < nvec; c += 32) {
       float w[8];
       load_router8<kF32>(a.router, static_cast<long long>(e) * D + c * 8, w);
 #pragma unroll
       for (int j = 0; j < kTok; ++j) {
-        if (t0 + j >= a.T) break;
-        const uint4 q = reinterpret_cast<const uint4*>(xs + j * D)[c];
-        const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+        uint4 q = make_uint4(0, 0, 0, 0);
+        if (j < ntok) q = *(reinterpret_cast<const uint4*>(x + j * a.ldx) + c);
+        const uint32_t v[4] = {q.x, q.y, q.z, q.w};
         float p = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p = fmaf(bf16_hi(x[i]), w[2 * i + 1], fmaf(bf16_lo(x[i]), w[2 * i], p));
+        for (int i = 0; i < 4; ++i) p = fmaf(bf16_hi(v[i]), w[2 * i + 1], fmaf(bf16_lo(v[i]), w[2 * i], p));
         const float y = p - comp[j], t = s[j] + y;
         comp[j] = (t - s[j]) - y;
         s[j] = t;
       }
+    }
+    if (!joined) {
+      asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+      joined = true;
     }
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
       double v = static_cast<double>(s[j]) - static_cast<double>(comp[j]);
 #pragma unroll
       for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-      if (lane == 0)
+      if (lane == 0 && j < ntok)
         asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(remote + (j * kMoeMaxExperts + e) * 8), "d"(v) : "memory");
     }
   }
+  if (!joined) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 
-  // this CTA's eighth of the token rows, in FP16 times 2^(14 - exponent of the largest)
+  // this CTA's eighth of the token rows, in FP16 times 2^(14 - exponent of the row's largest)
 #pragma unroll
   for (int j = 0; j < kTok; ++j) {
-    if (t0 + j >= a.T) break;
-    uint32_t m = 0;
+    uint32_t top = 0;
+    if (j < ntok) {
+#pragma unroll 1
+      for (int c = tid; c < nvec; c += kThreads) {
+        const uint4 q = *(reinterpret_cast<const uint4*>(x + j * a.ldx) + c);
+        const uint32_t m = __vmaxu2(__vmaxu2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu),
+                                    __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu));
+        top = max(top, max(m << 16, m & 0xFFFF0000u));
+      }
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if (lane == 0) part[j][warp] = top;
+  }
+  __syncthreads();
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) m = max(m, part[j][i]);
-    const int ex = exponent_of(m);
+  for (int j = 0; j < kTok; ++j) {
+    if (j >= ntok) break;
+    const int ex = exponent_of(__reduce_max_sync(0xFFFFFFFFu, part[j][lane & (kWarps - 1)]));
     const float up = pow2(14 - ex);
+#pragma unroll 1
     for (int c = rank * kThreads + tid; c < nvec; c += kRouteCtas * kThreads) {
-      const uint4 q = reinterpret_cast<const uint4*>(xs + j * D)[c];
-      const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+      const uint4 q = *(reinterpret_cast<const uint4*>(x + j * a.ldx) + c);
+      const uint32_t v[4] = {q.x, q.y, q.z, q.w};
       uint32_t h[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) h[i] = f16x2_from_f32(bf16_lo(x[i]) * up, bf16_hi(x[i]) * up);
+      for (int i = 0; i < 4; ++i) h[i] = f16x2_from_f32(bf16_lo(v[i]) * up, bf16_hi(v[i]) * up);
       reinterpret_cast<uint4*>(a.xh + static_cast<long long>(t0 + j) * D)[c] = make_uint4(h[0], h[1], h[2], h[3]);
     }
     if (rank == 0 && tid == 0) a.xscale[t0 + j] = pow2(ex - 14);
   }
   cluster_barrier();
-  if (rank != 0 || warp >= kTok || t0 + warp >= a.T) return;
+  if (rank != 0 || warp >= ntok) return;
 
-  // top-k of one token by one warp: keys and scores in FP64, lane l holds experts l, l + 32, ...
-  constexpr int kPer = kMoeMaxExperts / 32;
-  const int t = t0 + warp;
-  double key[kPer], p[kPer];
-  const double kNone = -CUDART_INF;
-  double mx = kNone;
+  // top-k of one token by one warp; lane l looks after experts l, l + 32, ...
+  const int t = t0 + warp, E = a.E;
+  double* sc = score[warp];
+  unsigned long long* ks = key[warp];
+  double mx = -CUDART_INF, sum = 0.0;
+  if (!a.sigmoid) {
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) mx = fmax(mx, sc[e]);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = i * 32 + lane;
-    p[i] = e < a.E ? logits[warp][e] : kNone;
-    mx = fmax(mx, p[i]);
+    for (int o = 16; o; o >>= 1) mx = fmax(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) mx = fmax(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
-  double sum = 0.0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = i * 32 + lane;
-    if (i * 32 >= a.E) break;
-    const double l = p[i];
-    if (a.sigmoid) {
-      p[i] = 1.0 / (1.0 + exp(-l));
-    } else {
-      p[i] = e < a.E ? exp(l - mx) : 0.0;
-      sum += p[i];
-    }
-    key[i] = a.bias ? 0.0 : l;
+#pragma unroll 1
+  for (int e = lane; e < E; e += 32) {
+    const double l = sc[e], ex = exp(a.sigmoid ? -l : l - mx);
+    const double p = a.sigmoid ? 1.0 / (1.0 + ex) : ex;
+    sum += p;
+    sc[e] = p;
+    ks[e] = order_key(l);
   }
+  double norm = 1.0;
   if (!a.sigmoid) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    norm = 1.0 / sum;
   }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int e = i * 32 + lane;
-    if (i * 32 >= a.E) break;
-    if (!a.sigmoid) p[i] /= sum;
-    if (e < a.E && a.bias) key[i] = p[i] + static_cast<double>(__ldg(a.bias + e));
-    if (isnan(key[i])) key[i] = kNone;            // a score that is no number is picked last
+  if (a.bias) {
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) ks[e] = order_key(sc[e] * norm + static_cast<double>(__ldg(a.bias + e)));
   }
-  uint32_t used = 0;
+  auto scan = [&](unsigned long long& best, int& at) {
+    best = 0;
+    at = 0;
+#pragma unroll 1
+    for (int e = lane; e < E; e += 32) {
+      if (ks[e] > best) {                         // ties: the lowest index
+        best = ks[e];
+        at = e;
+      }
+    }
+  };
+  unsigned long long best;
+  int at, my_id = 0;
+  scan(best, at);
   double wsum = 0.0, mine = 0.0;                  // lane j keeps the j-th weight
-  int my_id = 0;
+#pragma unroll 1
   for (int j = 0; j < a.k; ++j) {
-    double best = kNone, bp = 0.0;
-    int bi = 0x7FFFFFFF;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int e = i * 32 + lane;
-      if (e < a.E && !(used >> i & 1) && (bi == 0x7FFFFFFF || key[i] > best)) {
-        best = key[i];
-        bi = e;
-        bp = p[i];
-      }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {                // ties: the lowest index
-      const double ob = __shfl_xor_sync(0xFFFFFFFFu, best, o), op = __shfl_xor_sync(0xFFFFFFFFu, bp, o);
-      const int oi = __shfl_xor_sync(0xFFFFFFFFu, bi, o);
-      if (oi != 0x7FFFFFFF && (bi == 0x7FFFFFFF || ob > best || (ob == best && oi < bi))) {
-        best = ob;
-        bi = oi;
-        bp = op;
-      }
-    }
-    if ((bi & 31) == lane) used |= 1u << (bi >> 5);
+    const uint32_t hi = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(best >> 32));
+    const uint32_t lo = __reduce_max_sync(0xFFFFFFFFu, static_cast<uint32_t>(best >> 32) == hi ? static_cast<uint32_t>(best) : 0u);
+    const bool top = best == ((static_cast<unsigned long long>(hi) << 32) | lo);
+    const int id = static_cast<int>(__reduce_min_sync(0xFFFFFFFFu, top ? static_cast<uint32_t>(at) : 0xFFFFFFFFu));
+    const double p = sc[id] * norm;
     if (lane == j) {
-      mine = bp;
-      my_id = bi;
+      mine = p;
+      my_id = id;
     }
-    wsum += bp;
+    wsum += p;
+    if (top && at == id) {
+      ks[id] = 0;
+      scan(best, at);
+    }
+    __syncwarp();
   }
   const int KT = a.k + a.shared;
   if (lane < KT) {
     float w = 1.0f;
-    int id = a.E + lane - a.k;                    // shared experts follow the routed ones
+    int id = E + lane - a.k;                      // shared experts follow the routed ones
     if (lane < a.k) {
       w = static_cast<float>((a.renorm ? mine / wsum : mine) * static_cast<double>(a.route_scale));
       id = my_id;
@@ -342,31 +345,31 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The weight bytes of one block of 128 along K: two 64-element runs of kTiles 8-row tiles.
-struct WBlock {
-  uint4 w[2][kTiles];
-};
-__device__ __forceinline__ uint4 ld_weight(const uint8_t* p) {
+// A warp's stream of weights: runs of 64 along K of kTiles 8-row tiles, copied to shared
+// memory kStages - 1 runs ahead.  A lane reads back only what it copied itself, so the
+// stream needs no barriers, and unlike registers its depth costs nothing: 16 warps of an SM
+// keep 96 KB in flight.  (Held in registers one block ahead, the kernels spilled and the up
+// kernel ran at a seventh of the memory rate.)
+constexpr int kStages = 4;
+constexpr int kRunBytes = kTiles * 512;
+constexpr int kStreamBytes = kWarps * kStages * kRunBytes;
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool in) {
+  const uint32_t n = in ? 16u : 0u;
+  asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
   uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
   return v;
 }
-// `row[i]`: this lane's row of tile i, or null past the matrix.
-__device__ __forceinline__ void load_wblock(WBlock& b, const uint8_t* const (&row)[kTiles], int k, int K) {
-#pragma unroll
-  for (int c = 0; c < 2; ++c)
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i)
-      b.w[c][i] = (row[i] && k + c * 64 < K) ? ld_weight(row[i] + k + c * 64) : make_uint4(0, 0, 0, 0);
-}
 
-// blk[i] += tokens x tile i over one 64-element run; lo/hi: 16 FP16 values of token rows g, g + 8.
-__device__ __forceinline__ void mma_run(float (&blk)[kTiles][4], const uint4 (&w)[kTiles], const uint32_t (&lo)[8],
+// blk[i] += tokens x tile i over one 64-element run (this lane's bytes at `stage`); lo/hi: 16 FP16 values of token rows g, g + 8.
+__device__ __forceinline__ void mma_run(float (&blk)[kTiles][4], uint32_t stage, const uint32_t (&lo)[8],
                                         const uint32_t (&hi)[8]) {
 #pragma unroll
   for (int i = 0; i < kTiles; ++i) {
-    const uint32_t q[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+    const uint4 w = lds128(stage + i * 512);
+    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j)
       mma16816(blk[i], lo[2 * j], hi[2 * j], lo[2 * j + 1], hi[2 * j + 1], f16x2_from_e4m3x2(q[j] & 0xFFFFu),
@@ -389,9 +392,11 @@ __device__ __forceinline__ void load_row16(uint32_t (&v)[8], const uint16_t* p) 
 
 // Item (expert, 16 hidden columns): two tiles of gate rows, the two tiles of the same up
 // rows.  The CTA's warps split D; their sums meet in shared memory, where one warp at a time
-// finishes an item while the others go on.  Items of one expert follow each other in a CTA,
-// so its token rows stay in L1.  More than 16 tokens of an expert take further passes over
-// the item's weights, which then come from L2.
+// finishes an item while the others go on.  The CTAs walk through the items side by side, so
+// that all of them read the same few megabytes at a time: with a run of items of its own for
+// each CTA, 1.4 GB of experts took twice as long (the pages of 296 places do not fit the
+// address caches).  More than 16 tokens of an expert take further passes over the item's
+// weights, which then come from L2.
 __global__ void __launch_bounds__(kThreads, 2)
 moe_up_kernel(const __grid_constant__ MoeArgs a) {
   __shared__ Lists l;
@@ -404,27 +409,49 @@ moe_up_kernel(const __grid_constant__ MoeArgs a) {
   const int KB = (D + 127) / 128, NB = (2 * F + 127) / 128, strips = F / 16;
   const int items = l.nact * strips;
   const int b0 = KB * warp / kWarps, b1 = KB * (warp + 1) / kWarps;
-  int it = static_cast<int>(static_cast<long long>(items) * blockIdx.x / gridDim.x);
-  const int it1 = static_cast<int>(static_cast<long long>(items) * (blockIdx.x + 1) / gridDim.x);
-  const uint8_t* row[kTiles];
+  const int stride = static_cast<int>(gridDim.x);
+  int it = static_cast<int>(blockIdx.x);
   // tile i: gate (0, 1) or up (2, 3) rows; a tile never crosses a block of 128 rows
   auto tile_row = [&](int item, int i) { return (i >> 1) * F + item % strips * 16 + (i & 1) * 8; };
-  auto set_rows = [&](int item) {
-    const uint8_t* W = a.w13 + static_cast<long long>(l.active[item / strips]) * 2 * F * D;
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) row[i] = W + static_cast<long long>(tile_row(item, i) + g) * D + t4 * 16;
+
+  extern __shared__ __align__(16) uint8_t stream[];
+  const uint32_t ring = smem_u32(stream) + warp * (kStages * kRunBytes) + lane * 16;
+  const int runs = 2 * (b1 - b0);
+  // where the copies are: item, pass, run of the warp's part of D
+  int ci = it, cp = 0, cr = 0, cslot = 0;
+  const uint8_t* cbase = nullptr;
+  auto seek = [&] {
+    cbase = a.w13 + (static_cast<long long>(l.active[ci / strips]) * 2 * F + ci % strips * 16 + g) * D + b0 * 128 + t4 * 16;
   };
-  WBlock next;
-  if (it < it1 && b0 < b1) {
-    set_rows(it);
-    load_wblock(next, row, b0 * 128, D - t4 * 16);
-  }
-  for (int p0 = 0, step = 0; it < it1; ++step) {
+  auto copy_run = [&] {
+    if (ci < items && runs) {
+      const bool in = b0 * 128 + cr * 64 + t4 * 16 < D;
+      const uint8_t* src = cbase + cr * 64;
+#pragma unroll
+      for (int i = 0; i < kTiles; ++i)
+        cp_async16_or_zero(ring + cslot * kRunBytes + i * 512,
+                           in ? src + static_cast<long long>((i >> 1) * F + (i & 1) * 8) * D : cbase, in);
+      if (++cr == runs) {
+        cr = 0;
+        cp += 16;
+        if (cp >= l.count[l.active[ci / strips]]) {
+          cp = 0;
+          if ((ci += stride) < items) seek();
+        }
+      }
+    }
+    cp_async_commit();
+    cslot = cslot + 1 == kStages ? 0 : cslot + 1;
+  };
+  if (ci < items) seek();
+#pragma unroll 1
+  for (int i = 0; i < kStages - 1; ++i) copy_run();
+  int slot = 0;
+  for (int p0 = 0, step = 0; it < items; ++step) {
     const int e = l.active[it / strips], f0 = it % strips * 16;
     const int cnt = min(16, l.count[e] - p0);
     const int* pairs = l.pairs + l.begin[e] + p0;
     const bool more = p0 + 16 < l.count[e];
-    const int it_next = more ? it : it + 1;
     const uint16_t* xlo = g < cnt ? a.xh + static_cast<long long>(pairs[g] / KT) * D + t4 * 16 : nullptr;
     const uint16_t* xhi = g + 8 < cnt ? a.xh + static_cast<long long>(pairs[g + 8] / KT) * D + t4 * 16 : nullptr;
     const float* S = a.s13 + static_cast<long long>(e) * NB * KB;
@@ -434,14 +461,8 @@ moe_up_kernel(const __grid_constant__ MoeArgs a) {
     float out[kTiles][4];
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) out[i][0] = out[i][1] = out[i][2] = out[i][3] = 0.0f;
+#pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-      const WBlock cur = next;
-      if (b + 1 < b1) {
-        load_wblock(next, row, (b + 1) * 128, D - t4 * 16);
-      } else if (it_next < it1) {
-        set_rows(it_next);
-        load_wblock(next, row, b0 * 128, D - t4 * 16);
-      }
       float blk[kTiles][4], s[kTiles];
 #pragma unroll
       for (int i = 0; i < kTiles; ++i) {
@@ -455,7 +476,10 @@ moe_up_kernel(const __grid_constant__ MoeArgs a) {
         uint32_t lo[8], hi[8];
         load_row16(lo, in && xlo ? xlo + k : nullptr);
         load_row16(hi, in && xhi ? xhi + k : nullptr);
-        mma_run(blk, cur.w[c], lo, hi);
+        cp_async_wait<kStages - 2>();
+        mma_run(blk, ring + slot * kRunBytes, lo, hi);
+        copy_run();                       // into the slot before this one, read by now
+        slot = slot + 1 == kStages ? 0 : slot + 1;
       }
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
@@ -510,7 +534,7 @@ moe_up_kernel(const __grid_constant__ MoeArgs a) {
       }
     }
     p0 = more ? p0 + 16 : 0;
-    it = it_next;
+    if (!more) it += stride;
   }
 }
 
@@ -533,11 +557,13 @@ __device__ __forceinline__ void load_hidden(uint32_t (&v)[8], const MoeArgs& a, 
 }
 
 // A cluster of `a.split` CTAs owns 32 output rows.  Unit (active expert, block of 128 along
-// F); a warp takes a run of units and adds each expert's weighted sums into its own
-// [tokens][32] array; the arrays are summed over warps and CTAs in order.
+// F); the units are dealt out in turn over the cluster's warps (so that all CTAs read the
+// same experts at a time, as in the up kernel).  A warp adds each expert's weighted sums
+// into its own [tokens][32] array; the arrays are summed over warps and CTAs in order.
 __global__ void __launch_bounds__(kThreads, 2)
 moe_down_kernel(const __grid_constant__ MoeArgs a) {
-  extern __shared__ __align__(16) float acc[];                 // [kWarps][T][kPitch]
+  extern __shared__ __align__(16) uint8_t stream[];            // the weight stream, then [kWarps][T][kPitch] sums
+  float* acc = reinterpret_cast<float*>(stream + kStreamBytes);
   constexpr int kRows = 8 * kTiles, kPitch = kRows + 1;
   __shared__ Lists l;
   griddep_launch_dependents();
@@ -551,44 +577,57 @@ moe_down_kernel(const __grid_constant__ MoeArgs a) {
   float* mine = acc + warp * T * kPitch;
 
   const int units = l.nact * KB, parts = a.split * kWarps, part = rank * kWarps + warp;
-  int u = static_cast<int>(static_cast<long long>(units) * part / parts);
-  const int u1 = static_cast<int>(static_cast<long long>(units) * (part + 1) / parts);
-  const uint8_t* row[kTiles];
-  auto set_rows = [&](int unit) {
-    const uint8_t* W = a.w2 + static_cast<long long>(l.active[unit / KB]) * D * F;
+  int u = part;
+  const uint32_t ring = smem_u32(stream) + warp * (kStages * kRunBytes) + lane * 16;
+  // where the copies are: unit, run of its block, the expert's first unit and pass
+  int cu = u, cr = 0, cseg = u, cp = 0, ce = 0, cslot = 0;
+  auto copy_run = [&] {
+    if (cu < units) {
+      if (cr == 0 && cu == cseg) ce = l.active[cu / KB];
+      const int k = cu % KB * 128 + cr * 64 + t4 * 16;
+      const uint8_t* src = a.w2 + (static_cast<long long>(ce) * D + n0 + g) * F + k;
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) {
-      const int n = n0 + i * 8 + g;
-      row[i] = n < D ? W + static_cast<long long>(n) * F + t4 * 16 : nullptr;
+      for (int i = 0; i < kTiles; ++i) {
+        const bool in = k < F && n0 + i * 8 < D;
+        cp_async16_or_zero(ring + cslot * kRunBytes + i * 512, in ? src + static_cast<long long>(i * 8) * F : a.w2, in);
+      }
+      if (cr ^= 1; cr == 0) {
+        const int ca = cu / KB;
+        cu += parts;
+        if (cu / KB != ca) {                    // the expert's units are through: again, or on
+          cp += 16;
+          if (cp < l.count[ce]) {
+            cu = cseg;
+          } else {
+            cp = 0;
+            cseg = cu;
+          }
+        }
+      }
     }
+    cp_async_commit();
+    cslot = cslot + 1 == kStages ? 0 : cslot + 1;
   };
-  // the weights do not depend on the kernels before: the first block is requested at once
-  WBlock next;
-  if (u < u1) {
-    set_rows(u);
-    load_wblock(next, row, u % KB * 128, F - t4 * 16);
-  }
+  // the weights do not depend on the kernels before: the first runs are requested at once
+#pragma unroll 1
+  for (int i = 0; i < kStages - 1; ++i) copy_run();
+  int slot = 0;
   griddep_wait();
-  for (int p0 = 0; u < u1;) {
-    const int e = l.active[u / KB], ba = u % KB, bb = min(KB, ba + u1 - u);
+  for (int p0 = 0; u < units;) {
+    const int act = u / KB, e = l.active[act];
     const int cnt = min(16, l.count[e] - p0);
     const int* pairs = l.pairs + l.begin[e] + p0;
     const bool more = p0 + 16 < l.count[e];
-    const int u_next = more ? u : u + bb - ba;
     const float* S = a.s2 + (static_cast<long long>(e) * NB + n0 / 128) * KB;      // 32 rows: one block of 128
     const int qlo = g < cnt ? pairs[g] : -1, qhi = g + 8 < cnt ? pairs[g + 8] : -1;
     const int elo = qlo >= 0 ? exponent_of(__ldcg(a.hmax + qlo)) : 0, ehi = qhi >= 0 ? exponent_of(__ldcg(a.hmax + qhi)) : 0;
     float out[kTiles][4];
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) out[i][0] = out[i][1] = out[i][2] = out[i][3] = 0.0f;
-    for (int b = ba; b < bb; ++b) {
-      const WBlock cur = next;
-      if (b + 1 < bb) {
-        load_wblock(next, row, (b + 1) * 128, F - t4 * 16);
-      } else if (u_next < u1) {
-        set_rows(u_next);
-        load_wblock(next, row, u_next % KB * 128, F - t4 * 16);
-      }
+    int v = u;
+#pragma unroll 1
+    for (; v < units && v / KB == act; v += parts) {
+      const int b = v - act * KB;
       const float s = __ldg(S + b);
       float blk[kTiles][4];
 #pragma unroll
@@ -599,7 +638,10 @@ moe_down_kernel(const __grid_constant__ MoeArgs a) {
         uint32_t lo[8], hi[8];
         load_hidden(lo, a, k < F ? qlo : -1, k, elo, strips);
         load_hidden(hi, a, k < F ? qhi : -1, k, ehi, strips);
-        mma_run(blk, cur.w[c], lo, hi);
+        cp_async_wait<kStages - 2>();
+        mma_run(blk, ring + slot * kRunBytes, lo, hi);
+        copy_run();                       // into the slot before this one, read by now
+        slot = slot + 1 == kStages ? 0 : slot + 1;
       }
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
@@ -620,7 +662,7 @@ moe_down_kernel(const __grid_constant__ MoeArgs a) {
     }
     __syncwarp();
     p0 = more ? p0 + 16 : 0;
-    u = u_next;
+    if (!more) u = v;
   }
   __syncthreads();
   if (a.split > 1) cluster_barrier();
@@ -652,13 +694,7 @@ struct MoeSetup {
   std::once_flag once;
   cudaError_t err = cudaSuccess;
 };
-constexpr int kRouteSmemMax = 4 * BILOCO_MOE_MAX_D * 2, kDownSmemMax = kWarps * kMoeMaxTokens * (8 * kTiles + 1) * 4;
-
-template <int kTok, bool kF32>
-cudaError_t raise_route() {
-  return cudaFuncSetAttribute(moe_route_kernel<kTok, kF32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              kRouteSmemMax / 4 * kTok);
-}
+constexpr int kDownSmemMax = kStreamBytes + kWarps * kMoeMaxTokens * (8 * kTiles + 1) * 4;
 
 }  // namespace
 
@@ -687,38 +723,34 @@ cudaError_t launch_fp8_moe(MoeArgs& a, cudaStream_t s) {
   if (dev >= kMaxDevices) return cudaErrorInvalidDevice;
   MoeSetup& d = setups[dev];
   std::call_once(d.once, [&] {
-    const cudaError_t r[] = {raise_route<1, false>(), raise_route<1, true>(), raise_route<4, false>(),
-                             raise_route<4, true>(),
-                             cudaFuncSetAttribute(moe_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                  kDownSmemMax)};
-    for (cudaError_t v : r)
-      if (v != cudaSuccess) d.err = v;
+    d.err = cudaFuncSetAttribute(moe_up_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes);
+    if (d.err == cudaSuccess)
+      d.err = cudaFuncSetAttribute(moe_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDownSmemMax);
   });
   if (d.err != cudaSuccess) return d.err;
 
   // up to 16 tokens a cluster each (128 CTAs); above, four tokens share a cluster's reads of the router
   const int tok = a.T <= 16 ? 1 : 4;
   const unsigned grid = static_cast<unsigned>((a.T + tok - 1) / tok * kRouteCtas);
-  const size_t sm = static_cast<size_t>(tok) * a.D * 2;
   if (tok == 1)
-    e = a.router_f32 ? launch_pdl(moe_route_kernel<1, true>, grid, kThreads, sm, kRouteCtas, s, a)
-                     : launch_pdl(moe_route_kernel<1, false>, grid, kThreads, sm, kRouteCtas, s, a);
+    e = a.router_f32 ? launch_pdl(moe_route_kernel<1, true>, grid, kThreads, 0, kRouteCtas, s, a)
+                     : launch_pdl(moe_route_kernel<1, false>, grid, kThreads, 0, kRouteCtas, s, a);
   else
-    e = a.router_f32 ? launch_pdl(moe_route_kernel<4, true>, grid, kThreads, sm, kRouteCtas, s, a)
-                     : launch_pdl(moe_route_kernel<4, false>, grid, kThreads, sm, kRouteCtas, s, a);
+    e = a.router_f32 ? launch_pdl(moe_route_kernel<4, true>, grid, kThreads, 0, kRouteCtas, s, a)
+                     : launch_pdl(moe_route_kernel<4, false>, grid, kThreads, 0, kRouteCtas, s, a);
   if (e != cudaSuccess) return e;
 
   const int slots = 2 * num_sms();
   const int experts = min(a.T * a.k, a.E) + a.shared;
   const int items = experts * (a.F / 16);
-  e = launch_pdl(moe_up_kernel, static_cast<unsigned>(min(slots, items)), kThreads, 0, 1, s, a);
+  e = launch_pdl(moe_up_kernel, static_cast<unsigned>(min(slots, items)), kThreads, kStreamBytes, 1, s, a);
   if (e != cudaSuccess) return e;
 
   // the cluster of an output strip is as large as one wave of CTAs allows
   const int rows = (a.D + 8 * kTiles - 1) / (8 * kTiles);
   a.split = max(1, min(8, slots / rows));
   return launch_pdl(moe_down_kernel, static_cast<unsigned>(rows * a.split), kThreads,
-                    static_cast<size_t>(kWarps) * a.T * (8 * kTiles + 1) * 4, static_cast<unsigned>(a.split), s, a);
+                    kStreamBytes + static_cast<size_t>(kWarps) * a.T * (8 * kTiles + 1) * 4, static_cast<unsigned>(a.split), s, a);
 }
 
 }  // namespace biloco
