@@ -354,7 +354,7 @@ int biloco_block_norm(const void *y_bf16, long long ldy, const void *h, long lon
  *            weights [2F][D]): rows 0..F-1 are W1 (gate), F..2F-1 are W3 (up)
  *   w2       [E + shared][D][F] codes and scales
  *   shared   the last `shared` experts serve every token with weight 1
- *   y_bf16   out [T][D]; ids out [T][k] int, weights out [T][k] float, in the order picked
+ *   y_bf16   out [T][D], 8-byte aligned; ids out [T][k] int, weights out [T][k] float, in the order picked
  *   workspace  device memory of at least biloco_fp8_moe_workspace_bytes (256-byte aligned),
  *            owned by the caller; its contents do not matter before the call and are of no
  *            use after it.  Two calls that may overlap need two of them.
@@ -364,7 +364,7 @@ int biloco_block_norm(const void *y_bf16, long long ldy, const void *h, long lon
  * is picked last.  The products are FP16 x E4M3 with FP32 sums: rows of x are scaled into
  * FP16 exactly (BF16 values more than 2^29 below the row's largest lose bits), the hidden
  * values are rounded to FP16.  A token with an infinity or NaN spoils only its own row.
- * Three kernels with programmatic dependent launch; w2 may be read before the kernel before
+ * Four kernels with programmatic dependent launch; w2 may be read before the kernel before
  * them on the stream has ended (see biloco_gemm on what must not write the weight).
  * The result depends only on the operands and the shape.
  */

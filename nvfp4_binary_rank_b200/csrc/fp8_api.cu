@@ -132,7 +132,7 @@ int biloco_fp8_moe(const void* x_bf16, long long ldx, const void* router, int ro
   if (!need || E < 1 || E > BILOCO_MOE_MAX_E || k > E || ldx < D || ldx % 8) return BILOCO_ERR_SHAPE;
   if (workspace_bytes < need) return BILOCO_ERR_ARG;
   if (off(x_bf16, 16) || off(router, 16) || off(bias, 4) || off(w13_codes, 16) || off(w13_scales, 4) ||
-      off(w2_codes, 16) || off(w2_scales, 4) || off(y_bf16, 2) || off(ids, 4) || off(weights, 4) || off(workspace, 256))
+      off(w2_codes, 16) || off(w2_scales, 4) || off(y_bf16, 8) || off(ids, 4) || off(weights, 4) || off(workspace, 256))
     return BILOCO_ERR_ALIGN;
   const int d = check_device();
   if (d) return d;

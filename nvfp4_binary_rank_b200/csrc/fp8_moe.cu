@@ -16,12 +16,12 @@
 // Within a block of 128 along K the order of the terms is free, so lane t of a quad takes 16
 // consecutive elements of a 64-element run for both operands and no data is exchanged.
 //
-// Three kernels on one stream, each launched while the one before it ends:
-//   route  scores in FP32 with compensated sums, top-k, the token rows in FP16
-//   up     per (expert, 16 hidden columns): gate and up rows over the whole of D, split
-//          over the CTA's warps; h as FP16 with a scale per 16 columns and the row's maximum
-//   down   per 32 output rows: all experts' h; the (expert, block) units are dealt out
-//          evenly over a cluster's warps, whose sums are added in a fixed order
+// Four kernels on one stream, each launched while the one before it ends:
+//   route    scores in FP32 with compensated sums, top-k, the token rows in FP16
+//   product  (up) per (expert, 16 hidden columns): gate and up rows over the whole of D, split
+//            over the CTA's warps; h in FP16 with an exponent per 8 columns, and the row's maximum
+//   product  (down) per (expert, 64 output rows): each (token, expert) pair's share of y in FP32
+//   combine  the shares of a token added in the order its experts were picked
 // Nothing is added by atomics but a maximum, so the result does not depend on timing.
 #include <algorithm>
 #include <cstdint>
@@ -298,6 +298,18 @@ struct Lists {
 // Every CTA groups the (token, expert) pairs by expert for itself.
 __device__ __forceinline__ void build_lists(Lists& l, const MoeArgs& a) {
   const int tid = threadIdx.x, n = a.E + a.shared, P = a.T * (a.k + a.shared);
+  if (a.T == 1) {                                  // every pair is an expert of its own
+    if (tid < P) {
+      const int e = __ldcg(a.pair_id + tid);
+      l.active[tid] = e;
+      l.pairs[tid] = tid;
+      l.begin[e] = tid;
+      l.count[e] = 1;
+    }
+    if (tid == 0) l.nact = P;
+    __syncthreads();
+    return;
+  }
   for (int e = tid; e < n; e += kThreads) l.count[e] = 0;
   __syncthreads();
   int pos[kMoeMaxPairs / kThreads], id[kMoeMaxPairs / kThreads];
@@ -377,64 +389,83 @@ __device__ __forceinline__ void mma_run(float (&blk)[kTiles][4], uint32_t stage,
   }
 }
 
-__device__ __forceinline__ void load_row16(uint32_t (&v)[8], const uint16_t* p) {
-  if (p) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p), b = *(reinterpret_cast<const uint4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0;
-  }
+// 32 bytes into v where `has`; v keeps its zeros elsewhere (no select per register).
+__device__ __forceinline__ void load_run(uint32_t (&v)[8], const uint16_t* p, bool has) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %9, 0;\n\t"
+      "@q ld.global.v4.u32 {%0,%1,%2,%3}, [%8];\n\t"
+      "@q ld.global.v4.u32 {%4,%5,%6,%7}, [%8+16];\n\t}"
+      : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])
+      : "l"(p), "r"(static_cast<uint32_t>(has)));
 }
 
-// ------------------------------------------------------------------ up
+// Scales 16 hidden values, stored relative to the exponents `e` of their two strips of 8, to the row's.
+__device__ __forceinline__ void scale_hidden(uint32_t (&v)[8], int2 e, int row_exp) {
+  // a strip's exponent is at most the row's; lanes without values have any, and stay zero
+  const float f0 = pow2(min(max(e.x - row_exp + 14, -30), 14)), f1 = pow2(min(max(e.y - row_exp + 14, -30), 14));
+  const uint32_t h0 = f16x2_from_f32(f0, f0), h1 = f16x2_from_f32(f1, f1);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) asm("mul.rn.f16x2 %0, %0, %1;" : "+r"(v[j]) : "r"(j < 4 ? h0 : h1));
+}
 
-// Item (expert, 16 hidden columns): two tiles of gate rows, the two tiles of the same up
-// rows.  The CTA's warps split D; their sums meet in shared memory, where one warp at a time
-// finishes an item while the others go on.  The CTAs walk through the items side by side, so
-// that all of them read the same few megabytes at a time: with a run of items of its own for
-// each CTA, 1.4 GB of experts took twice as long (the pages of 296 places do not fit the
-// address caches).  More than 16 tokens of an expert take further passes over the item's
-// weights, which then come from L2.
+// The products of both layers.  A row group is four tiles: for the up layer the gate and the
+// up rows of 16 hidden columns, for the down layer 32 output rows.  An item is an expert and
+// kGroups row groups; kSplit warps share a group's blocks along K and meet in shared memory,
+// the CTAs walk through the items side by side, so that all of them read the same few
+// megabytes at a time: with a run of items of its own for each CTA, 1.4 GB of experts took
+// twice as long (the pages of 296 places do not fit the address caches).  More than 16 tokens
+// of an expert take further passes over the item's weights, which then come from L2.
+template <bool kUp>
 __global__ void __launch_bounds__(kThreads, 2)
-moe_up_kernel(const __grid_constant__ MoeArgs a) {
+moe_product_kernel(const __grid_constant__ MoeArgs a) {
+  constexpr int kSplit = kUp ? 8 : 4, kGroups = kWarps / kSplit;
+  extern __shared__ __align__(16) uint8_t stream[];
   __shared__ Lists l;
   __shared__ float4 red[2][kWarps][kTiles][32];
-  griddep_wait();
-  griddep_launch_dependents();      // after the wait: the next kernel may read the route's results at once
+  if (kUp) griddep_wait();
+  // in the up kernel after the wait: the down kernel may then read the route's results at once
+  griddep_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
   build_lists(l, a);
-  const int D = a.D, F = a.F, KT = a.k + a.shared;
-  const int KB = (D + 127) / 128, NB = (2 * F + 127) / 128, strips = F / 16;
-  const int items = l.nact * strips;
-  const int b0 = KB * warp / kWarps, b1 = KB * (warp + 1) / kWarps;
-  const int stride = static_cast<int>(gridDim.x);
-  int it = static_cast<int>(blockIdx.x);
-  // tile i: gate (0, 1) or up (2, 3) rows; a tile never crosses a block of 128 rows
-  auto tile_row = [&](int item, int i) { return (i >> 1) * F + item % strips * 16 + (i & 1) * 8; };
+  const int K = kUp ? a.D : a.F, F = a.F, D = a.D, KT = a.k + a.shared;
+  const int KB = (K + 127) / 128, NB = ((kUp ? 2 * F : D) + 127) / 128;
+  const int groups = kUp ? F / 16 : (D + 31) / 32, per = (groups + kGroups - 1) / kGroups;   // items of an expert
+  const int items = l.nact * per, stride = static_cast<int>(gridDim.x);
+  const int sub = warp / kSplit, kp = warp % kSplit;
+  const int b0 = KB * kp / kSplit, b1 = KB * (kp + 1) / kSplit, runs = 2 * (b1 - b0);
+  const uint8_t* const W = kUp ? a.w13 : a.w2;
+  const uint16_t* const A = kUp ? a.xh : a.h;
 
-  extern __shared__ __align__(16) uint8_t stream[];
+  // ---- the weight stream
   const uint32_t ring = smem_u32(stream) + warp * (kStages * kRunBytes) + lane * 16;
-  const int runs = 2 * (b1 - b0);
-  // where the copies are: item, pass, run of the warp's part of D
-  int ci = it, cp = 0, cr = 0, cslot = 0;
+  int ci = static_cast<int>(blockIdx.x), cp = 0, cr = 0, cslot = 0, ccount = 0;
   const uint8_t* cbase = nullptr;
+  int o1 = 8 * K, o2 = kUp ? F * K : 16 * K, o3 = o2 + 8 * K;      // offsets of tiles 1 to 3
   auto seek = [&] {
-    cbase = a.w13 + (static_cast<long long>(l.active[ci / strips]) * 2 * F + ci % strips * 16 + g) * D + b0 * 128 + t4 * 16;
+    const int act = ci / per, e = l.active[act], grp = min((ci - act * per) * kGroups + sub, groups - 1);
+    ccount = l.count[e];
+    const int n = grp * (kUp ? 16 : 32);
+    cbase = W + (static_cast<long long>(e) * (kUp ? 2 * F : D) + n + g) * K + b0 * 128 + t4 * 16;
+    if (!kUp && n + 32 > D) {                       // the matrix ends inside the group: a tile twice
+      o2 = o3 = o1;
+    } else if (!kUp) {
+      o2 = 16 * K;
+      o3 = 24 * K;
+    }
   };
   auto copy_run = [&] {
     if (ci < items && runs) {
-      const bool in = b0 * 128 + cr * 64 + t4 * 16 < D;
-      const uint8_t* src = cbase + cr * 64;
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i)
-        cp_async16_or_zero(ring + cslot * kRunBytes + i * 512,
-                           in ? src + static_cast<long long>((i >> 1) * F + (i & 1) * 8) * D : cbase, in);
+      const bool in = b0 * 128 + cr * 64 + t4 * 16 < K;
+      const uint8_t* src = in ? cbase + cr * 64 : cbase;
+      const uint32_t dst = ring + cslot * kRunBytes;
+      cp_async16_or_zero(dst, src, in);
+      cp_async16_or_zero(dst + 512, src + o1, in);
+      cp_async16_or_zero(dst + 1024, src + o2, in);
+      cp_async16_or_zero(dst + 1536, src + o3, in);
       if (++cr == runs) {
         cr = 0;
         cp += 16;
-        if (cp >= l.count[l.active[ci / strips]]) {
+        if (cp >= ccount) {
           cp = 0;
           if ((ci += stride) < items) seek();
         }
@@ -446,90 +477,151 @@ moe_up_kernel(const __grid_constant__ MoeArgs a) {
   if (ci < items) seek();
 #pragma unroll 1
   for (int i = 0; i < kStages - 1; ++i) copy_run();
+  // the down layer's weights do not depend on the kernels before, its activations do
+  if (!kUp) griddep_wait();
+
   int slot = 0;
-  for (int p0 = 0, step = 0; it < items; ++step) {
-    const int e = l.active[it / strips], f0 = it % strips * 16;
+  for (int it = static_cast<int>(blockIdx.x), p0 = 0, step = 0; it < items; ++step) {
+    const int act = it / per, e = l.active[act], grp0 = (it - act * per) * kGroups;
     const int cnt = min(16, l.count[e] - p0);
     const int* pairs = l.pairs + l.begin[e] + p0;
-    const bool more = p0 + 16 < l.count[e];
-    const uint16_t* xlo = g < cnt ? a.xh + static_cast<long long>(pairs[g] / KT) * D + t4 * 16 : nullptr;
-    const uint16_t* xhi = g + 8 < cnt ? a.xh + static_cast<long long>(pairs[g + 8] / KT) * D + t4 * 16 : nullptr;
-    const float* S = a.s13 + static_cast<long long>(e) * NB * KB;
-    const float* srow[kTiles];
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) srow[i] = S + tile_row(it, i) / 128 * KB;
+    const bool more = p0 + 16 < l.count[e], wide = cnt > 8;
+    const bool haslo = g < cnt, hashi = g + 8 < cnt;
+    const int qlo = haslo ? pairs[g] : 0, qhi = hashi ? pairs[g + 8] : 0;
+    const long long rlo = kUp ? qlo / KT : qlo, rhi = kUp ? qhi / KT : qhi;
+    const uint16_t* plo = A + rlo * K + b0 * 128 + t4 * 16;
+    const uint16_t* phi = A + rhi * K + b0 * 128 + t4 * 16;
+    const int2* xlo = nullptr;
+    const int2* xhi = nullptr;
+    int elo = 0, ehi = 0;
+    if (!kUp) {
+      xlo = reinterpret_cast<const int2*>(a.hexp + rlo * (F / 8)) + (b0 * 8 + t4);
+      xhi = reinterpret_cast<const int2*>(a.hexp + rhi * (F / 8)) + (b0 * 8 + t4);
+      elo = exponent_of(__ldcg(a.hmax + qlo));
+      ehi = exponent_of(__ldcg(a.hmax + qhi));
+    }
+    const int n = min(grp0 + sub, groups - 1) * (kUp ? 16 : 32);
+    const float* S = (kUp ? a.s13 : a.s2) + (static_cast<long long>(e) * NB + n / 128) * KB;
+    const float* S2 = kUp ? a.s13 + (static_cast<long long>(e) * NB + (F + n) / 128) * KB : S;
     float out[kTiles][4];
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) out[i][0] = out[i][1] = out[i][2] = out[i][3] = 0.0f;
+    // activations of token rows g (and of g + 8 where there are more than eight), a run ahead
+    uint32_t lo[8], hi[8], lo2[8], hi2[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) lo[j] = hi[j] = lo2[j] = hi2[j] = 0;
+    int2 xe = make_int2(0, 0), xe2 = xe, xf = xe, xf2 = xe;
+    auto fetch = [&](uint32_t (&l8)[8], uint32_t (&h8)[8], int2& el, int2& eh, int r) {
+      const bool in = b0 * 128 + r * 64 + t4 * 16 < K;
+      load_run(l8, plo + r * 64, haslo && in);
+      if (!kUp && haslo && in) el = __ldcg(xlo + r * 4);
+      if (wide) {
+        load_run(h8, phi + r * 64, hashi && in);
+        if (!kUp && hashi && in) eh = __ldcg(xhi + r * 4);
+      }
+    };
+    // a run's values are scaled in place; past K they must be the zeros again
+    auto take = [&](uint32_t (&l8)[8], uint32_t (&h8)[8], int2 el, int2 eh, float (&blk)[kTiles][4]) {
+      if (!kUp) {
+        scale_hidden(l8, el, elo);
+        if (wide) scale_hidden(h8, eh, ehi);
+      }
+      cp_async_wait<kStages - 2>();
+      mma_run(blk, ring + slot * kRunBytes, l8, h8);
+      copy_run();                       // into the slot before this one, read by now
+      slot = slot + 1 == kStages ? 0 : slot + 1;
+    };
+    float s_next = 0.0f, u_next = 0.0f;
+    if (runs) {
+      fetch(lo, hi, xe, xf, 0);
+      s_next = __ldg(S + b0);
+      u_next = __ldg(S2 + b0);
+    }
 #pragma unroll 1
     for (int b = b0; b < b1; ++b) {
-      float blk[kTiles][4], s[kTiles];
+      const float sg = s_next, su = u_next;
+      float blk[kTiles][4];
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        blk[i][0] = blk[i][1] = blk[i][2] = blk[i][3] = 0.0f;
-        s[i] = __ldg(srow[i] + b);
-      }
+      for (int i = 0; i < kTiles; ++i) blk[i][0] = blk[i][1] = blk[i][2] = blk[i][3] = 0.0f;
+      const int r = 2 * (b - b0);
+      if (b + 1 == KB && (K & 127)) {   // the last block may end anywhere: no values of the run before
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int k = b * 128 + c * 64;
-        const bool in = k + t4 * 16 < D;
-        uint32_t lo[8], hi[8];
-        load_row16(lo, in && xlo ? xlo + k : nullptr);
-        load_row16(hi, in && xhi ? xhi + k : nullptr);
-        cp_async_wait<kStages - 2>();
-        mma_run(blk, ring + slot * kRunBytes, lo, hi);
-        copy_run();                       // into the slot before this one, read by now
-        slot = slot + 1 == kStages ? 0 : slot + 1;
+        for (int j = 0; j < 8; ++j) lo2[j] = hi2[j] = 0;
       }
+      fetch(lo2, hi2, xe2, xf2, r + 1);
+      take(lo, hi, xe, xf, blk);
+      if (b + 1 < b1) {
+        if (b + 2 == KB && (K & 127)) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) lo[j] = hi[j] = 0;
+        }
+        fetch(lo, hi, xe, xf, r + 2);
+        s_next = __ldg(S + b + 1);
+        u_next = __ldg(S2 + b + 1);
+      }
+      take(lo2, hi2, xe2, xf2, blk);
 #pragma unroll
       for (int i = 0; i < kTiles; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) out[i][j] = fmaf(blk[i][j], s[i], out[i][j]);
+        for (int j = 0; j < 4; ++j) out[i][j] = fmaf(blk[i][j], kUp && i >= 2 ? su : sg, out[i][j]);
     }
     // Two buffers: the barrier of the step between orders a buffer's next use after its reads.
     float4(*sums)[kTiles][32] = red[step & 1];
 #pragma unroll
     for (int i = 0; i < kTiles; ++i) sums[warp][i][lane] = make_float4(out[i][0], out[i][1], out[i][2], out[i][3]);
     __syncthreads();
-    if (warp == (step & (kWarps - 1))) {
-      float v[2][4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
+    if (kUp) {
+      // two warps in turn take eight hidden columns each: tile i of the gate, tile 2 + i of the up rows
+      const int i = (warp - 2 * step) & (kWarps - 1);
+      if (i < 2) {
         float gs[4] = {0, 0, 0, 0}, us[4] = {0, 0, 0, 0};
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
+        for (int w = 0; w < kSplit; ++w) {
           const float4 p = sums[w][i][lane], q = sums[w][2 + i][lane];
           gs[0] += p.x; gs[1] += p.y; gs[2] += p.z; gs[3] += p.w;
           us[0] += q.x; us[1] += q.y; us[2] += q.z; us[3] += q.w;
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = g + (j >> 1) * 8;
-          const float xs = r < cnt ? a.xscale[pairs[r] / KT] : 0.0f;
-          const float gv = gs[j] * xs, uv = us[j] * xs;
-          v[i][j] = gv / (1.0f + expf(-gv)) * uv;
+        for (int half = 0; half < 2; ++half) {
+          const bool has = half ? hashi : haslo;
+          const int q = half ? qhi : qlo;
+          const float xs = has ? a.xscale[half ? rhi : rlo] : 0.0f;
+          float v[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float gv = gs[half * 2 + j] * xs, uv = us[half * 2 + j] * xs;
+            v[j] = gv / (1.0f + expf(-gv)) * uv;
+          }
+          uint32_t m = max(__float_as_uint(v[0]) & 0x7FFFFFFFu, __float_as_uint(v[1]) & 0x7FFFFFFFu);
+          m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+          m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+          if (has) {
+            const int ex = exponent_of(m), f = n + i * 8;
+            const float up = pow2(-ex);
+            *reinterpret_cast<uint32_t*>(a.h + static_cast<long long>(q) * F + f + 2 * t4) = f16x2_from_f32(v[0] * up, v[1] * up);
+            if (t4 == 0) {
+              a.hexp[static_cast<long long>(q) * (F / 8) + f / 8] = ex;
+              atomicMax(a.hmax + q, m);
+            }
+          }
         }
+      }
+    } else {
+      // warp (group, tile): the sums of the group's kSplit warps
+      const int i = warp % kTiles, row = (grp0 + warp / kTiles) * 32 + i * 8 + 2 * t4;
+      float v[4] = {0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < kSplit; ++w) {
+        const float4 p = sums[warp / kTiles * kSplit + w][i][lane];
+        v[0] += p.x; v[1] += p.y; v[2] += p.z; v[3] += p.w;
       }
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        const int r = g + half * 8;
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 2; ++j) m = max(m, __float_as_uint(v[i][half * 2 + j]) & 0x7FFFFFFFu);
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-        m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-        if (r < cnt) {
-          const int q = pairs[r], ex = exponent_of(m);
-          const float up = pow2(-ex);
-          uint32_t* h = reinterpret_cast<uint32_t*>(a.h + static_cast<long long>(q) * F + f0 + 2 * t4);
-          h[0] = f16x2_from_f32(v[0][half * 2] * up, v[0][half * 2 + 1] * up);
-          h[4] = f16x2_from_f32(v[1][half * 2] * up, v[1][half * 2 + 1] * up);
-          if (t4 == 0) {
-            a.hexp[static_cast<long long>(q) * strips + f0 / 16] = ex;
-            atomicMax(a.hmax + q, m);
-          }
+        if ((half ? hashi : haslo) && row < D) {
+          const int q = half ? qhi : qlo;
+          const float w = __ldcg(a.pair_w + q) * pow2((half ? ehi : elo) - 14);
+          *reinterpret_cast<float2*>(a.share + static_cast<long long>(q) * D + row) =
+              make_float2(w * v[half * 2], w * v[half * 2 + 1]);
         }
       }
     }
@@ -538,152 +630,25 @@ moe_up_kernel(const __grid_constant__ MoeArgs a) {
   }
 }
 
-// ------------------------------------------------------------------ down
+// ------------------------------------------------------------------ combine
 
-// 16 hidden values of pair q from column k (one strip), brought to the row's exponent.
-__device__ __forceinline__ void load_hidden(uint32_t (&v)[8], const MoeArgs& a, int q, int k, int row_exp, int strips) {
-  if (q < 0) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0;
-    return;
-  }
-  const uint4* p = reinterpret_cast<const uint4*>(a.h + static_cast<long long>(q) * a.F + k);
-  const uint4 x = __ldcg(p), y = __ldcg(p + 1);
-  const int d = max(__ldcg(a.hexp + static_cast<long long>(q) * strips + k / 16) - row_exp + 14, -30);
-  const uint32_t f = f16x2_from_f32(pow2(d), pow2(d));
-  const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-  for (int j = 0; j < 8; ++j) asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(v[j]) : "r"(w[j]), "r"(f));
-}
-
-// A cluster of `a.split` CTAs owns 32 output rows.  Unit (active expert, block of 128 along
-// F); the units are dealt out in turn over the cluster's warps (so that all CTAs read the
-// same experts at a time, as in the up kernel).  A warp adds each expert's weighted sums
-// into its own [tokens][32] array; the arrays are summed over warps and CTAs in order.
-__global__ void __launch_bounds__(kThreads, 2)
-moe_down_kernel(const __grid_constant__ MoeArgs a) {
-  extern __shared__ __align__(16) uint8_t stream[];            // the weight stream, then [kWarps][T][kPitch] sums
-  float* acc = reinterpret_cast<float*>(stream + kStreamBytes);
-  constexpr int kRows = 8 * kTiles, kPitch = kRows + 1;
-  __shared__ Lists l;
+// y[t] = the sum of its pairs' shares, in order; four columns a thread.
+__global__ void __launch_bounds__(kThreads)
+moe_combine_kernel(const __grid_constant__ MoeArgs a) {
   griddep_launch_dependents();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-  const int rank = a.split > 1 ? static_cast<int>(cta_rank()) : 0;
-  const int D = a.D, F = a.F, T = a.T, KT = a.k + a.shared;
-  const int KB = (F + 127) / 128, NB = (D + 127) / 128, strips = F / 16;
-  const int n0 = static_cast<int>(blockIdx.x) / a.split * kRows;
-  for (int i = tid; i < kWarps * T * kPitch; i += kThreads) acc[i] = 0.0f;
-  build_lists(l, a);                        // the route kernel ended before this one could start
-  float* mine = acc + warp * T * kPitch;
-
-  const int units = l.nact * KB, parts = a.split * kWarps, part = rank * kWarps + warp;
-  int u = part;
-  const uint32_t ring = smem_u32(stream) + warp * (kStages * kRunBytes) + lane * 16;
-  // where the copies are: unit, run of its block, the expert's first unit and pass
-  int cu = u, cr = 0, cseg = u, cp = 0, ce = 0, cslot = 0;
-  auto copy_run = [&] {
-    if (cu < units) {
-      if (cr == 0 && cu == cseg) ce = l.active[cu / KB];
-      const int k = cu % KB * 128 + cr * 64 + t4 * 16;
-      const uint8_t* src = a.w2 + (static_cast<long long>(ce) * D + n0 + g) * F + k;
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        const bool in = k < F && n0 + i * 8 < D;
-        cp_async16_or_zero(ring + cslot * kRunBytes + i * 512, in ? src + static_cast<long long>(i * 8) * F : a.w2, in);
-      }
-      if (cr ^= 1; cr == 0) {
-        const int ca = cu / KB;
-        cu += parts;
-        if (cu / KB != ca) {                    // the expert's units are through: again, or on
-          cp += 16;
-          if (cp < l.count[ce]) {
-            cu = cseg;
-          } else {
-            cp = 0;
-            cseg = cu;
-          }
-        }
-      }
-    }
-    cp_async_commit();
-    cslot = cslot + 1 == kStages ? 0 : cslot + 1;
-  };
-  // the weights do not depend on the kernels before: the first runs are requested at once
-#pragma unroll 1
-  for (int i = 0; i < kStages - 1; ++i) copy_run();
-  int slot = 0;
   griddep_wait();
-  for (int p0 = 0; u < units;) {
-    const int act = u / KB, e = l.active[act];
-    const int cnt = min(16, l.count[e] - p0);
-    const int* pairs = l.pairs + l.begin[e] + p0;
-    const bool more = p0 + 16 < l.count[e];
-    const float* S = a.s2 + (static_cast<long long>(e) * NB + n0 / 128) * KB;      // 32 rows: one block of 128
-    const int qlo = g < cnt ? pairs[g] : -1, qhi = g + 8 < cnt ? pairs[g + 8] : -1;
-    const int elo = qlo >= 0 ? exponent_of(__ldcg(a.hmax + qlo)) : 0, ehi = qhi >= 0 ? exponent_of(__ldcg(a.hmax + qhi)) : 0;
-    float out[kTiles][4];
-#pragma unroll
-    for (int i = 0; i < kTiles; ++i) out[i][0] = out[i][1] = out[i][2] = out[i][3] = 0.0f;
-    int v = u;
-#pragma unroll 1
-    for (; v < units && v / KB == act; v += parts) {
-      const int b = v - act * KB;
-      const float s = __ldg(S + b);
-      float blk[kTiles][4];
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i) blk[i][0] = blk[i][1] = blk[i][2] = blk[i][3] = 0.0f;
-#pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int k = b * 128 + c * 64 + t4 * 16;
-        uint32_t lo[8], hi[8];
-        load_hidden(lo, a, k < F ? qlo : -1, k, elo, strips);
-        load_hidden(hi, a, k < F ? qhi : -1, k, ehi, strips);
-        cp_async_wait<kStages - 2>();
-        mma_run(blk, ring + slot * kRunBytes, lo, hi);
-        copy_run();                       // into the slot before this one, read by now
-        slot = slot + 1 == kStages ? 0 : slot + 1;
-      }
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) out[i][j] = fmaf(blk[i][j], s, out[i][j]);
-    }
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int q = half ? qhi : qlo;
-      if (q < 0) continue;
-      const float w = __ldcg(a.pair_w + q) * pow2((half ? ehi : elo) - 14);
-      float* y = mine + q / KT * kPitch + 2 * t4;
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        y[i * 8] = fmaf(w, out[i][half * 2], y[i * 8]);
-        y[i * 8 + 1] = fmaf(w, out[i][half * 2 + 1], y[i * 8 + 1]);
-      }
-    }
-    __syncwarp();
-    p0 = more ? p0 + 16 : 0;
-    if (!more) u = v;
+  const int KT = a.k + a.shared, quads = a.D / 4, i = static_cast<int>(blockIdx.x) * kThreads + threadIdx.x;
+  if (i >= a.T * quads) return;
+  const int t = i / quads, c = i % quads;
+  const float4* p = reinterpret_cast<const float4*>(a.share + static_cast<long long>(t) * KT * a.D) + c;
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+  for (int j = 0; j < KT; ++j) {
+    const float4 v = __ldcg(p + static_cast<long long>(j) * quads);
+    s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
   }
-  __syncthreads();
-  if (a.split > 1) cluster_barrier();
-  const uint32_t base = smem_u32(acc);
-  for (int i = rank * kThreads + tid; i < T * kRows; i += a.split * kThreads) {
-    const int t = i / kRows, r = i % kRows;
-    float sum = 0.0f;
-    for (int q = 0; q < a.split; ++q) {
-      float v[kWarps];
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const uint32_t at = base + ((w * T + t) * kPitch + r) * 4;
-        if (a.split > 1) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[w]) : "r"(mapa_u32(at, q)));
-        else v[w] = acc[(w * T + t) * kPitch + r];
-      }
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) sum += v[w];
-    }
-    if (n0 + r < D) a.y[static_cast<long long>(t) * D + n0 + r] = static_cast<uint16_t>(bf16x2_from_f32(sum, 0.0f));
-  }
-  if (a.split > 1) cluster_barrier();       // the others may still be reading this CTA's sums
+  *reinterpret_cast<uint2*>(a.y + static_cast<long long>(t) * a.D + c * 4) =
+      make_uint2(bf16x2_from_f32(s.x, s.y), bf16x2_from_f32(s.z, s.w));
 }
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
@@ -694,7 +659,6 @@ struct MoeSetup {
   std::once_flag once;
   cudaError_t err = cudaSuccess;
 };
-constexpr int kDownSmemMax = kStreamBytes + kWarps * kMoeMaxTokens * (8 * kTiles + 1) * 4;
 
 }  // namespace
 
@@ -708,10 +672,11 @@ size_t moe_carve(MoeArgs& a, uint8_t* base) {
   take(a.pair_id, P * 4);
   take(a.pair_w, P * 4);
   take(a.hmax, P * 4);
-  take(a.hexp, P * (a.F / 16) * 4);
+  take(a.hexp, P * (a.F / 8) * 4);
   take(a.xh, static_cast<size_t>(a.T) * a.D * 2);
   take(a.xscale, static_cast<size_t>(a.T) * 4);
   take(a.h, P * a.F * 2);
+  take(a.share, P * a.D * 4);
   return at;
 }
 
@@ -723,9 +688,9 @@ cudaError_t launch_fp8_moe(MoeArgs& a, cudaStream_t s) {
   if (dev >= kMaxDevices) return cudaErrorInvalidDevice;
   MoeSetup& d = setups[dev];
   std::call_once(d.once, [&] {
-    d.err = cudaFuncSetAttribute(moe_up_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes);
+    d.err = cudaFuncSetAttribute(moe_product_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes);
     if (d.err == cudaSuccess)
-      d.err = cudaFuncSetAttribute(moe_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kDownSmemMax);
+      d.err = cudaFuncSetAttribute(moe_product_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes);
   });
   if (d.err != cudaSuccess) return d.err;
 
@@ -742,15 +707,16 @@ cudaError_t launch_fp8_moe(MoeArgs& a, cudaStream_t s) {
 
   const int slots = 2 * num_sms();
   const int experts = min(a.T * a.k, a.E) + a.shared;
-  const int items = experts * (a.F / 16);
-  e = launch_pdl(moe_up_kernel, static_cast<unsigned>(min(slots, items)), kThreads, kStreamBytes, 1, s, a);
+  const long long up = static_cast<long long>(experts) * (a.F / 16);
+  e = launch_pdl(moe_product_kernel<true>, static_cast<unsigned>(std::min<long long>(slots, up)), kThreads, kStreamBytes, 1,
+                 s, a);
   if (e != cudaSuccess) return e;
-
-  // the cluster of an output strip is as large as one wave of CTAs allows
-  const int rows = (a.D + 8 * kTiles - 1) / (8 * kTiles);
-  a.split = max(1, min(8, slots / rows));
-  return launch_pdl(moe_down_kernel, static_cast<unsigned>(rows * a.split), kThreads,
-                    kStreamBytes + static_cast<size_t>(kWarps) * a.T * (8 * kTiles + 1) * 4, static_cast<unsigned>(a.split), s, a);
+  const long long down = static_cast<long long>(experts) * ((a.D + 63) / 64);
+  e = launch_pdl(moe_product_kernel<false>, static_cast<unsigned>(std::min<long long>(slots, down)), kThreads, kStreamBytes,
+                 1, s, a);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(moe_combine_kernel, static_cast<unsigned>((a.T * (a.D / 4) + kThreads - 1) / kThreads), kThreads, 0, 1,
+                    s, a);
 }
 
 }  // namespace biloco

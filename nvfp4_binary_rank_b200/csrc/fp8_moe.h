@@ -31,12 +31,13 @@ struct MoeArgs {
   int* pair_id;            // [T][k + shared] expert of each (token, choice) pair
   float* pair_w;           // its weight
   uint32_t* hmax;          // bits of the largest |h| of a pair's hidden row
-  int* hexp;               // [pairs][F/16] exponent that a strip of h is stored relative to
+  int* hexp;               // [pairs][F/8] exponent that 8 columns of h are stored relative to
   uint16_t* xh;            // [T][D] FP16 token rows, scaled
   float* xscale;           // [T] what to multiply them by
   uint16_t* h;             // [pairs][F] FP16
+  float* share;            // [pairs][D] what a pair adds to y
   long long ldx;
-  int T, D, F, E, k, shared, split;
+  int T, D, F, E, k, shared;
   bool sigmoid, renorm, router_f32;
   float route_scale;
 };
