@@ -46,6 +46,7 @@ namespace {
 constexpr int kThreads = 256, kWarps = 8;
 constexpr int kTiles = 4;                 // 8-row weight tiles of one item
 constexpr int kRouteCtas = 8;             // cluster of the route kernel
+constexpr int kAhead = 5;                 // router pieces of 256 columns a lane has in flight
 
 __device__ __forceinline__ uint32_t mapa_u32(uint32_t addr, uint32_t rank) {
   uint32_t r;
@@ -117,19 +118,35 @@ __device__ __forceinline__ unsigned long long order_key(double v) {
 template <int kTok, bool kF32>
 __global__ void __launch_bounds__(kThreads)
 moe_route_kernel(const __grid_constant__ MoeArgs a) {
+  extern __shared__ __align__(16) uint8_t rows[];                       // [kTok][D] bf16
   __shared__ double score[kTok][kMoeMaxExperts];                        // the scores, then the weights
   __shared__ unsigned long long key[kTok][kMoeMaxExperts];
   __shared__ uint32_t part[kTok][kWarps];
   griddep_launch_dependents();
   griddep_wait();
-  // the first CTA's shared memory may be written once that CTA runs
-  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(cta_rank());
   const int t0 = static_cast<int>(blockIdx.x) / kRouteCtas * kTok;
   const int D = a.D, nvec = D / 8, ntok = min(kTok, a.T - t0);
-  const uint16_t* x = a.x + t0 * a.ldx;
-  bool joined = false;
+  uint4* const xs = reinterpret_cast<uint4*>(rows);
+
+  // the token rows into shared memory, and each row's largest magnitude
+#pragma unroll
+  for (int j = 0; j < kTok; ++j) {
+    const uint4* x = reinterpret_cast<const uint4*>(a.x + (t0 + min(j, ntok - 1)) * a.ldx);
+    uint32_t top = 0;
+#pragma unroll 4
+    for (int c = tid; c < nvec; c += kThreads) {
+      const uint4 q = x[c];
+      xs[j * nvec + c] = q;
+      const uint32_t m = __vmaxu2(__vmaxu2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu),
+                                  __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu));
+      top = max(top, max(m << 16, m & 0xFFFF0000u));
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, top);
+    if (lane == 0) part[j][warp] = top;
+  }
+  cluster_barrier();            // also: the first CTA runs, so its shared memory may be written
 
   // scores: a warp takes whole experts; sums of eight products, compensated over a lane's
   // eights (Kahan), in FP64 over the lanes
@@ -139,26 +156,30 @@ moe_route_kernel(const __grid_constant__ MoeArgs a) {
     float s[kTok], comp[kTok];
 #pragma unroll
     for (int j = 0; j < kTok; ++j) s[j] = comp[j] = 0.0f;
-#pragma unroll 4
-    for (int c = lane; c < nvec; c += 32) {
-      float w[8];
-      load_router8<kF32>(a.router, static_cast<long long>(e) * D + c * 8, w);
+#pragma unroll 1
+    for (int c0 = lane; c0 < nvec; c0 += 32 * kAhead) {
+      float w[kAhead][8];                             // the loads of kAhead pieces in flight
 #pragma unroll
-      for (int j = 0; j < kTok; ++j) {
-        uint4 q = make_uint4(0, 0, 0, 0);
-        if (j < ntok) q = *(reinterpret_cast<const uint4*>(x + j * a.ldx) + c);
-        const uint32_t v[4] = {q.x, q.y, q.z, q.w};
-        float p = 0.0f;
+      for (int u = 0; u < kAhead; ++u) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p = fmaf(bf16_hi(v[i]), w[2 * i + 1], fmaf(bf16_lo(v[i]), w[2 * i], p));
-        const float y = p - comp[j], t = s[j] + y;
-        comp[j] = (t - s[j]) - y;
-        s[j] = t;
+        for (int i = 0; i < 8; ++i) w[u][i] = 0.0f;
+        if (c0 + 32 * u < nvec) load_router8<kF32>(a.router, static_cast<long long>(e) * D + (c0 + 32 * u) * 8, w[u]);
       }
-    }
-    if (!joined) {
-      asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-      joined = true;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+#pragma unroll
+        for (int j = 0; j < kTok; ++j) {
+          const uint4 q = xs[j * nvec + min(c0 + 32 * u, nvec - 1)];
+          const uint32_t v[4] = {q.x, q.y, q.z, q.w};
+          float p = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p = fmaf(bf16_hi(v[i]), w[u][2 * i + 1], fmaf(bf16_lo(v[i]), w[u][2 * i], p));
+          if (c0 + 32 * u >= nvec) p = 0.0f;
+          const float y = p - comp[j], t = s[j] + y;
+          comp[j] = (t - s[j]) - y;
+          s[j] = t;
+        }
+      }
     }
 #pragma unroll
     for (int j = 0; j < kTok; ++j) {
@@ -169,25 +190,8 @@ moe_route_kernel(const __grid_constant__ MoeArgs a) {
         asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(remote + (j * kMoeMaxExperts + e) * 8), "d"(v) : "memory");
     }
   }
-  if (!joined) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 
   // this CTA's eighth of the token rows, in FP16 times 2^(14 - exponent of the row's largest)
-#pragma unroll
-  for (int j = 0; j < kTok; ++j) {
-    uint32_t top = 0;
-    if (j < ntok) {
-#pragma unroll 1
-      for (int c = tid; c < nvec; c += kThreads) {
-        const uint4 q = *(reinterpret_cast<const uint4*>(x + j * a.ldx) + c);
-        const uint32_t m = __vmaxu2(__vmaxu2(q.x & 0x7FFF7FFFu, q.y & 0x7FFF7FFFu),
-                                    __vmaxu2(q.z & 0x7FFF7FFFu, q.w & 0x7FFF7FFFu));
-        top = max(top, max(m << 16, m & 0xFFFF0000u));
-      }
-    }
-    top = __reduce_max_sync(0xFFFFFFFFu, top);
-    if (lane == 0) part[j][warp] = top;
-  }
-  __syncthreads();
 #pragma unroll
   for (int j = 0; j < kTok; ++j) {
     if (j >= ntok) break;
@@ -195,7 +199,7 @@ moe_route_kernel(const __grid_constant__ MoeArgs a) {
     const float up = pow2(14 - ex);
 #pragma unroll 1
     for (int c = rank * kThreads + tid; c < nvec; c += kRouteCtas * kThreads) {
-      const uint4 q = *(reinterpret_cast<const uint4*>(x + j * a.ldx) + c);
+      const uint4 q = xs[j * nvec + c];
       const uint32_t v[4] = {q.x, q.y, q.z, q.w};
       uint32_t h[4];
 #pragma unroll
@@ -688,21 +692,28 @@ cudaError_t launch_fp8_moe(MoeArgs& a, cudaStream_t s) {
   if (dev >= kMaxDevices) return cudaErrorInvalidDevice;
   MoeSetup& d = setups[dev];
   std::call_once(d.once, [&] {
-    d.err = cudaFuncSetAttribute(moe_product_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes);
-    if (d.err == cudaSuccess)
-      d.err = cudaFuncSetAttribute(moe_product_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes);
+    auto raise = [&](auto* kernel, int bytes) {
+      if (d.err == cudaSuccess) d.err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    };
+    raise(moe_route_kernel<1, false>, BILOCO_MOE_MAX_D * 2);
+    raise(moe_route_kernel<1, true>, BILOCO_MOE_MAX_D * 2);
+    raise(moe_route_kernel<4, false>, 4 * BILOCO_MOE_MAX_D * 2);
+    raise(moe_route_kernel<4, true>, 4 * BILOCO_MOE_MAX_D * 2);
+    raise(moe_product_kernel<true>, kStreamBytes);
+    raise(moe_product_kernel<false>, kStreamBytes);
   });
   if (d.err != cudaSuccess) return d.err;
 
   // up to 16 tokens a cluster each (128 CTAs); above, four tokens share a cluster's reads of the router
   const int tok = a.T <= 16 ? 1 : 4;
   const unsigned grid = static_cast<unsigned>((a.T + tok - 1) / tok * kRouteCtas);
+  const size_t sm = static_cast<size_t>(tok) * a.D * 2;
   if (tok == 1)
-    e = a.router_f32 ? launch_pdl(moe_route_kernel<1, true>, grid, kThreads, 0, kRouteCtas, s, a)
-                     : launch_pdl(moe_route_kernel<1, false>, grid, kThreads, 0, kRouteCtas, s, a);
+    e = a.router_f32 ? launch_pdl(moe_route_kernel<1, true>, grid, kThreads, sm, kRouteCtas, s, a)
+                     : launch_pdl(moe_route_kernel<1, false>, grid, kThreads, sm, kRouteCtas, s, a);
   else
-    e = a.router_f32 ? launch_pdl(moe_route_kernel<4, true>, grid, kThreads, 0, kRouteCtas, s, a)
-                     : launch_pdl(moe_route_kernel<4, false>, grid, kThreads, 0, kRouteCtas, s, a);
+    e = a.router_f32 ? launch_pdl(moe_route_kernel<4, true>, grid, kThreads, sm, kRouteCtas, s, a)
+                     : launch_pdl(moe_route_kernel<4, false>, grid, kThreads, sm, kRouteCtas, s, a);
   if (e != cudaSuccess) return e;
 
   const int slots = 2 * num_sms();
