@@ -379,17 +379,23 @@ __device__ __forceinline__ uint4 lds128(uint32_t at) {
   return v;
 }
 
-// blk[i] += tokens x tile i over one 64-element run (this lane's bytes at `stage`); lo/hi: 16 FP16 values of token rows g, g + 8.
-__device__ __forceinline__ void mma_run(float (&blk)[kTiles][4], uint32_t stage, const uint32_t (&lo)[8],
-                                        const uint32_t (&hi)[8]) {
+// One 64-element run: the weight tiles at `stage` (this lane's bytes) against eight tokens, and
+// against eight more where kWide.  Tiles 2i and 2i + 1 are the 16 rows of one product, so a
+// thread gets weight rows g and g + 8 and tokens 2 t and 2 t + 1.
+template <bool kWide>
+__device__ __forceinline__ void mma_run(float (&b0)[2][4], float (&b1)[2][4], uint32_t stage, const uint32_t (&x0)[8],
+                                        const uint32_t (&x1)[8]) {
 #pragma unroll
-  for (int i = 0; i < kTiles; ++i) {
-    const uint4 w = lds128(stage + i * 512);
-    const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+  for (int i = 0; i < 2; ++i) {
+    const uint4 wa = lds128(stage + i * 1024), wb = lds128(stage + i * 1024 + 512);
+    const uint32_t p[4] = {wa.x, wa.y, wa.z, wa.w}, q[4] = {wb.x, wb.y, wb.z, wb.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      mma16816(blk[i], lo[2 * j], hi[2 * j], lo[2 * j + 1], hi[2 * j + 1], f16x2_from_e4m3x2(q[j] & 0xFFFFu),
-               f16x2_from_e4m3x2(q[j] >> 16));
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t a0 = f16x2_from_e4m3x2(p[j] & 0xFFFFu), a2 = f16x2_from_e4m3x2(p[j] >> 16);
+      const uint32_t a1 = f16x2_from_e4m3x2(q[j] & 0xFFFFu), a3 = f16x2_from_e4m3x2(q[j] >> 16);
+      mma16816(b0[i], a0, a1, a2, a3, x0[2 * j], x0[2 * j + 1]);
+      if (kWide) mma16816(b1[i], a0, a1, a2, a3, x1[2 * j], x1[2 * j + 1]);
+    }
   }
 }
 
@@ -485,150 +491,175 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
   if (!kUp) griddep_wait();
 
   int slot = 0;
-  for (int it = static_cast<int>(blockIdx.x), p0 = 0, step = 0; it < items; ++step) {
-    const int act = it / per, e = l.active[act], grp0 = (it - act * per) * kGroups;
-    const int cnt = min(16, l.count[e] - p0);
-    const int* pairs = l.pairs + l.begin[e] + p0;
-    const bool more = p0 + 16 < l.count[e], wide = cnt > 8;
-    const bool haslo = g < cnt, hashi = g + 8 < cnt;
-    const int qlo = haslo ? pairs[g] : 0, qhi = hashi ? pairs[g + 8] : 0;
-    const long long rlo = kUp ? qlo / KT : qlo, rhi = kUp ? qhi / KT : qhi;
-    const uint16_t* plo = A + rlo * K + b0 * 128 + t4 * 16;
-    const uint16_t* phi = A + rhi * K + b0 * 128 + t4 * 16;
-    const int2* xlo = nullptr;
-    const int2* xhi = nullptr;
-    int elo = 0, ehi = 0;
-    if (!kUp) {
-      xlo = reinterpret_cast<const int2*>(a.hexp + rlo * (F / 8)) + (b0 * 8 + t4);
-      xhi = reinterpret_cast<const int2*>(a.hexp + rhi * (F / 8)) + (b0 * 8 + t4);
-      elo = exponent_of(__ldcg(a.hmax + qlo));
-      ehi = exponent_of(__ldcg(a.hmax + qhi));
+  // One pass over an item for `cnt` tokens, at most 8 or (kWide) 16.
+  auto pass = [&](auto wide_t, int e, int grp0, const int* pairs, int cnt, float4 (*sums)[kTiles][32], int step) {
+    constexpr bool kWide = decltype(wide_t)::value;
+    constexpr int kHalves = kWide ? 2 : 1;
+    // this lane's token of either eight, as the products' second operand
+    const uint16_t* px[2];
+    const int2* pe[2];
+    bool has[2];
+    int rexp[2];
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h) {
+      has[h] = h * 8 + g < cnt;
+      const int q = has[h] ? pairs[h * 8 + g] : 0;
+      const long long r = kUp ? q / KT : q;
+      px[h] = A + r * K + b0 * 128 + t4 * 16;
+      if (!kUp) {
+        pe[h] = reinterpret_cast<const int2*>(a.hexp + r * (F / 8)) + (b0 * 8 + t4);
+        rexp[h] = exponent_of(__ldcg(a.hmax + q));
+      }
     }
     const int n = min(grp0 + sub, groups - 1) * (kUp ? 16 : 32);
     const float* S = (kUp ? a.s13 : a.s2) + (static_cast<long long>(e) * NB + n / 128) * KB;
     const float* S2 = kUp ? a.s13 + (static_cast<long long>(e) * NB + (F + n) / 128) * KB : S;
-    float out[kTiles][4];
+    float out[2][2][4];
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) out[i][0] = out[i][1] = out[i][2] = out[i][3] = 0.0f;
-    // activations of token rows g (and of g + 8 where there are more than eight), a run ahead
-    uint32_t lo[8], hi[8], lo2[8], hi2[8];
+    for (int h = 0; h < kHalves; ++h)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) lo[j] = hi[j] = lo2[j] = hi2[j] = 0;
-    int2 xe = make_int2(0, 0), xe2 = xe, xf = xe, xf2 = xe;
-    auto fetch = [&](uint32_t (&l8)[8], uint32_t (&h8)[8], int2& el, int2& eh, int r) {
-      const bool in = b0 * 128 + r * 64 + t4 * 16 < K;
-      load_run(l8, plo + r * 64, haslo && in);
-      if (!kUp && haslo && in) el = __ldcg(xlo + r * 4);
-      if (wide) {
-        load_run(h8, phi + r * 64, hashi && in);
-        if (!kUp && hashi && in) eh = __ldcg(xhi + r * 4);
+      for (int i = 0; i < 2; ++i) out[h][i][0] = out[h][i][1] = out[h][i][2] = out[h][i][3] = 0.0f;
+    // Activations of a block: two runs of the first eight tokens a block ahead, of the others
+    // when they are needed.
+    struct Acts {
+      uint32_t x[2][8];
+      int2 e[2];
+      float s, s2;
+    };
+    auto clear = [](uint32_t (&v)[8]) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0;
+    };
+    Acts even, odd;
+    clear(even.x[0]);
+    clear(even.x[1]);
+    clear(odd.x[0]);
+    clear(odd.x[1]);
+    even.e[0] = even.e[1] = odd.e[0] = odd.e[1] = make_int2(0, 0);
+    auto fetch = [&](Acts& f, int b) {
+      const bool tail = b + 1 == KB && (K & 127);     // the last block may end anywhere
+      f.s = __ldg(S + b);
+      f.s2 = kUp ? __ldg(S2 + b) : 0.0f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = 2 * (b - b0) + c;
+        const bool in = !tail || b * 128 + c * 64 + t4 * 16 < K;
+        if (tail) clear(f.x[c]);
+        load_run(f.x[c], px[0] + r * 64, has[0] && in);
+        if (!kUp && has[0] && in) f.e[c] = __ldcg(pe[0] + r * 4);
       }
     };
-    // a run's values are scaled in place; past K they must be the zeros again
-    auto take = [&](uint32_t (&l8)[8], uint32_t (&h8)[8], int2 el, int2 eh, float (&blk)[kTiles][4]) {
-      if (!kUp) {
-        scale_hidden(l8, el, elo);
-        if (wide) scale_hidden(h8, eh, ehi);
-      }
-      cp_async_wait<kStages - 2>();
-      mma_run(blk, ring + slot * kRunBytes, l8, h8);
-      copy_run();                       // into the slot before this one, read by now
-      slot = slot + 1 == kStages ? 0 : slot + 1;
-    };
-    float s_next = 0.0f, u_next = 0.0f;
-    if (runs) {
-      fetch(lo, hi, xe, xf, 0);
-      s_next = __ldg(S + b0);
-      u_next = __ldg(S2 + b0);
-    }
-#pragma unroll 1
-    for (int b = b0; b < b1; ++b) {
-      const float sg = s_next, su = u_next;
-      float blk[kTiles][4];
+    auto block = [&](Acts& cur, Acts& next, int b) {
+      uint32_t y[8];
+      float k0[2][4], k1[2][4];
+      if (kWide) clear(y);
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i) blk[i][0] = blk[i][1] = blk[i][2] = blk[i][3] = 0.0f;
-      const int r = 2 * (b - b0);
-      if (b + 1 == KB && (K & 127)) {   // the last block may end anywhere: no values of the run before
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) lo2[j] = hi2[j] = 0;
-      }
-      fetch(lo2, hi2, xe2, xf2, r + 1);
-      take(lo, hi, xe, xf, blk);
-      if (b + 1 < b1) {
-        if (b + 2 == KB && (K & 127)) {
+        for (int j = 0; j < 4; ++j) k0[i][j] = k1[i][j] = 0.0f;
+      if (b + 1 < b1) fetch(next, b + 1);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) lo[j] = hi[j] = 0;
+      for (int c = 0; c < 2; ++c) {
+        if (kWide) {
+          const int r = 2 * (b - b0) + c;
+          const bool in = b * 128 + c * 64 + t4 * 16 < K;
+          if (c == 1 && !in) clear(y);
+          int2 ye = make_int2(0, 0);
+          load_run(y, px[1] + r * 64, has[1] && in);
+          if (!kUp && has[1] && in) ye = __ldcg(pe[1] + r * 4);
+          if (!kUp) scale_hidden(y, ye, rexp[1]);
         }
-        fetch(lo, hi, xe, xf, r + 2);
-        s_next = __ldg(S + b + 1);
-        u_next = __ldg(S2 + b + 1);
+        if (!kUp) scale_hidden(cur.x[c], cur.e[c], rexp[0]);
+        cp_async_wait<kStages - 2>();
+        mma_run<kWide>(k0, k1, ring + slot * kRunBytes, cur.x[c], y);
+        copy_run();                       // into the slot before this one, read by now
+        slot = slot + 1 == kStages ? 0 : slot + 1;
       }
-      take(lo2, hi2, xe2, xf2, blk);
 #pragma unroll
-      for (int i = 0; i < kTiles; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) out[i][j] = fmaf(blk[i][j], kUp && i >= 2 ? su : sg, out[i][j]);
+        for (int j = 0; j < 4; ++j) {
+          out[0][i][j] = fmaf(k0[i][j], kUp && i ? cur.s2 : cur.s, out[0][i][j]);
+          if (kWide) out[1][i][j] = fmaf(k1[i][j], kUp && i ? cur.s2 : cur.s, out[1][i][j]);
+        }
+    };
+    if (runs) fetch(even, b0);
+#pragma unroll 1
+    for (int b = b0; b < b1; b += 2) {
+      block(even, odd, b);
+      if (b + 1 < b1) block(odd, even, b + 1);
     }
-    // Two buffers: the barrier of the step between orders a buffer's next use after its reads.
-    float4(*sums)[kTiles][32] = red[step & 1];
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) sums[warp][i][lane] = make_float4(out[i][0], out[i][1], out[i][2], out[i][3]);
+    for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        sums[warp][h * 2 + i][lane] = make_float4(out[h][i][0], out[h][i][1], out[h][i][2], out[h][i][3]);
     __syncthreads();
     if (kUp) {
-      // two warps in turn take eight hidden columns each: tile i of the gate, tile 2 + i of the up rows
-      const int i = (warp - 2 * step) & (kWarps - 1);
-      if (i < 2) {
+      // a warp (in turn) for each eight tokens: product 0 are the gate rows, product 1 the up rows
+      const int h = (warp - 2 * step) & (kWarps - 1);
+      if (h < kHalves) {
         float gs[4] = {0, 0, 0, 0}, us[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < kSplit; ++w) {
-          const float4 p = sums[w][i][lane], q = sums[w][2 + i][lane];
+          const float4 p = sums[w][2 * h][lane], q = sums[w][2 * h + 1][lane];
           gs[0] += p.x; gs[1] += p.y; gs[2] += p.z; gs[3] += p.w;
           us[0] += q.x; us[1] += q.y; us[2] += q.z; us[3] += q.w;
         }
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const bool has = half ? hashi : haslo;
-          const int q = half ? qhi : qlo;
-          const float xs = has ? a.xscale[half ? rhi : rlo] : 0.0f;
-          float v[2];
+        for (int j = 0; j < 2; ++j) {                   // tokens 2 t and 2 t + 1
+          const int r = h * 8 + 2 * t4 + j, q = r < cnt ? pairs[r] : 0;
+          const float xs = r < cnt ? a.xscale[q / KT] : 0.0f;
+          int top = 0;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const float gv = gs[half * 2 + j] * xs, uv = us[half * 2 + j] * xs;
-            v[j] = gv / (1.0f + expf(-gv)) * uv;
-          }
-          uint32_t m = max(__float_as_uint(v[0]) & 0x7FFFFFFFu, __float_as_uint(v[1]) & 0x7FFFFFFFu);
-          m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
-          m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
-          if (has) {
+          for (int i = 0; i < 2; ++i) {                 // hidden columns n + g and n + 8 + g
+            const float gv = gs[2 * i + j] * xs, uv = us[2 * i + j] * xs;
+            const float v = gv / (1.0f + expf(-gv)) * uv;
+            int m = static_cast<int>(__float_as_uint(v) & 0x7FFFFFFFu);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
             const int ex = exponent_of(m), f = n + i * 8;
-            const float up = pow2(-ex);
-            *reinterpret_cast<uint32_t*>(a.h + static_cast<long long>(q) * F + f + 2 * t4) = f16x2_from_f32(v[0] * up, v[1] * up);
-            if (t4 == 0) {
-              a.hexp[static_cast<long long>(q) * (F / 8) + f / 8] = ex;
-              atomicMax(a.hmax + q, m);
+            top = max(top, m);
+            if (r < cnt) {
+              a.h[static_cast<long long>(q) * F + f + g] = static_cast<uint16_t>(f16x2_from_f32(v * pow2(-ex), 0.0f));
+              if (g == 0) a.hexp[static_cast<long long>(q) * (F / 8) + f / 8] = ex;
             }
           }
+          if (r < cnt && g == 0) atomicMax(a.hmax + q, static_cast<uint32_t>(top));
         }
       }
     } else {
-      // warp (group, tile): the sums of the group's kSplit warps
-      const int i = warp % kTiles, row = (grp0 + warp / kTiles) * 32 + i * 8 + 2 * t4;
-      float v[4] = {0, 0, 0, 0};
+      // warp (group, eight tokens, product): the sums of the group's kSplit warps
+      const int h = (warp >> 1) & 1, i = warp & 1, row = (grp0 + warp / 4) * 32 + i * 16 + g;
+      if (h < kHalves) {
+        float v[4] = {0, 0, 0, 0};
 #pragma unroll
-      for (int w = 0; w < kSplit; ++w) {
-        const float4 p = sums[warp / kTiles * kSplit + w][i][lane];
-        v[0] += p.x; v[1] += p.y; v[2] += p.z; v[3] += p.w;
-      }
+        for (int w = 0; w < kSplit; ++w) {
+          const float4 p = sums[warp / 4 * kSplit + w][h * 2 + i][lane];
+          v[0] += p.x; v[1] += p.y; v[2] += p.z; v[3] += p.w;
+        }
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        if ((half ? hashi : haslo) && row < D) {
-          const int q = half ? qhi : qlo;
-          const float w = __ldcg(a.pair_w + q) * pow2((half ? ehi : elo) - 14);
-          *reinterpret_cast<float2*>(a.share + static_cast<long long>(q) * D + row) =
-              make_float2(w * v[half * 2], w * v[half * 2 + 1]);
+        for (int j = 0; j < 2; ++j) {
+          const int r = h * 8 + 2 * t4 + j;
+          if (r < cnt) {
+            const int q = pairs[r];
+            const float w = __ldcg(a.pair_w + q) * pow2(exponent_of(__ldcg(a.hmax + q)) - 14);
+            float* y = a.share + static_cast<long long>(q) * D + row;
+            if (row < D) y[0] = w * v[j];
+            if (row + 8 < D) y[8] = w * v[2 + j];
+          }
         }
       }
     }
+  };
+  for (int it = static_cast<int>(blockIdx.x), p0 = 0, step = 0; it < items; ++step) {
+    const int act = it / per, e = l.active[act], grp0 = (it - act * per) * kGroups;
+    const int cnt = min(16, l.count[e] - p0);
+    const int* pairs = l.pairs + l.begin[e] + p0;
+    const bool more = p0 + 16 < l.count[e];
+    // Two buffers: the barrier of the step between orders a buffer's next use after its reads.
+    if (cnt > 8) pass(std::true_type(), e, grp0, pairs, cnt, red[step & 1], step);
+    else pass(std::false_type(), e, grp0, pairs, cnt, red[step & 1], step);
     p0 = more ? p0 + 16 : 0;
     if (!more) it += stride;
   }
