@@ -7,9 +7,11 @@
 //
 // Bound by memory: y and h are read once, h' and x written once, and the row stays in
 // registers between the two norms.  A CTA takes a row at a time, a thread kVec pieces of eight
-// elements.  CTAs stay: each walks over rows with the loads of its next row under way while
-// the current one goes through its two sums.  y and h pass by L1, which so keeps the weights.
-// Measured at 8192 x 5120 with FP8 output (295 MB): one CTA per row 85 us, this NEW us.
+// elements, two at a time in packed FP32 arithmetic (with single operations the kernel issued
+// 696 instructions a warp and row and was bound by them).  CTAs stay: each walks over rows,
+// and the loads of its next row are under way from the middle of the current one, when the
+// registers of that are free.  y and h pass by L1, which so keeps the weights.
+// Measured at 8192 x 5120 with FP8 output (295 MB): one CTA per row 85 us, this 65 us.
 // Both sums of squares are FP32; x is computed from the unrounded h', so h' and x are each
 // rounded once.
 #include <algorithm>
@@ -27,21 +29,20 @@ namespace biloco {
 
 namespace {
 
-// Eight consecutive values as they lie in memory (BF16 or FP32), and widened.
+// Eight consecutive values as they lie in memory (BF16 or FP32), widened in pairs.
 template <bool kF32>
 struct Raw8 {
   uint4 q[kF32 ? 2 : 1];
   // weights and gates: cached
-  __device__ __forceinline__ void load(const void* p, long long at) {
+  __device__ __forceinline__ void load(const void* p, int at) {
     const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + at * (kF32 ? 4 : 2));
     q[0] = __ldg(s);
     if (kF32) q[kF32] = __ldg(s + 1);
   }
   // rows: read once, and perhaps written by this kernel (h' over h)
-  __device__ __forceinline__ void stream(const void* p, long long at) {
-    const uint8_t* s = static_cast<const uint8_t*>(p) + at * (kF32 ? 4 : 2);
-    take(q[0], s);
-    if (kF32) take(q[kF32], s + 16);
+  __device__ __forceinline__ void stream(const uint8_t* p) {
+    take(q[0], p);
+    if (kF32) take(q[kF32], p + 16);
   }
   static __device__ __forceinline__ void take(uint4& v, const uint8_t* p) {
     asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
@@ -51,19 +52,42 @@ struct Raw8 {
     q[0] = make_uint4(0, 0, 0, 0);
     if (kF32) q[kF32] = make_uint4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ float at(int j) const {
+  __device__ __forceinline__ uint64_t pair(int j) const {          // values 2 j and 2 j + 1
     if (kF32) {
-      const uint4& v = q[kF32 ? j >> 2 : 0];
-      return __uint_as_float((j & 3) == 0 ? v.x : (j & 3) == 1 ? v.y : (j & 3) == 2 ? v.z : v.w);
+      const uint4& v = q[kF32 ? j >> 1 : 0];
+      return (j & 1) ? f32x2_pack(v.z, v.w) : f32x2_pack(v.x, v.y);
     }
-    const uint32_t w = (j >> 1) == 0 ? q[0].x : (j >> 1) == 1 ? q[0].y : (j >> 1) == 2 ? q[0].z : q[0].w;
-    return (j & 1) ? bf16_hi(w) : bf16_lo(w);
+    const uint32_t w = j == 0 ? q[0].x : j == 1 ? q[0].y : j == 2 ? q[0].z : q[0].w;
+    return f32x2_pack(w << 16, w & 0xFFFF0000u);
   }
 };
 
-__device__ __forceinline__ uint4 to_bf16x8(const float (&v)[8]) {
-  return make_uint4(bf16x2_from_f32(v[0], v[1]), bf16x2_from_f32(v[2], v[3]), bf16x2_from_f32(v[4], v[5]),
-                    bf16x2_from_f32(v[6], v[7]));
+__device__ __forceinline__ uint64_t f32x2_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t both(float v) { return f32x2_pack(__float_as_uint(v), __float_as_uint(v)); }
+__device__ __forceinline__ void split(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint32_t pack_bf16(uint64_t v) {
+  float lo, hi;
+  split(v, lo, hi);
+  return bf16x2_from_f32(lo, hi);
+}
+// max(a, |lo|, |hi|), NaN if any is
+__device__ __forceinline__ float max_abs(float a, uint64_t v) {
+  float lo, hi;
+  split(v, lo, hi);
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(fabsf(lo)));
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(fabsf(hi)));
+  return a;
 }
 
 // Sum over the CTA; every thread gets it, summed in the same order.  `part` has one slot per
@@ -81,138 +105,142 @@ __device__ __forceinline__ float cta_sum(float v, float* part) {
   return v;
 }
 
-template <int kVec, int kMaxThreads, bool kAhead, bool kHf32, bool kWf32>
-__global__ void __launch_bounds__(kMaxThreads, kMaxThreads == 512 && !kHf32 ? 2 : 1)
+template <int kVec, int kMaxThreads, bool kHf32, bool kWf32>
+__global__ void __launch_bounds__(kMaxThreads, kMaxThreads == 512 ? 2 : 1)
 block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
   __shared__ float part[2][32];
-  const int D = a.D, nvec = D >> 3, step = static_cast<int>(gridDim.x);
-  auto piece = [&](int i) { return static_cast<int>(threadIdx.x + i * blockDim.x); };
-  struct Row {
-    Raw8<false> y[kVec];
-    Raw8<kHf32> h[kVec];
-  };
-  auto load_row = [&](Row& r, int m) {
+  const int D = a.D, nvec = D >> 3;
+  constexpr int kHb = kHf32 ? 4 : 2;
+  int at[kVec];                                // first element of this thread's pieces
+  bool in[kVec];
+  Raw8<false> y[kVec];
+  Raw8<kHf32> h[kVec];
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int c = static_cast<int>(threadIdx.x + i * blockDim.x);
+    in[i] = c < nvec;
+    at[i] = c * 8;
+    y[i].zero();                               // pieces past the row's end stay zero
+    h[i].zero();
+  }
+  auto load_row = [&](int m) {
+    const uint8_t* py = reinterpret_cast<const uint8_t*>(a.y) + m * a.ldy * 2;
+    const uint8_t* ph = static_cast<const uint8_t*>(a.h) + m * a.ldh * kHb;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      r.y[i].zero();
-      r.h[i].zero();
-      if (piece(i) < nvec) {
-        if (a.y) r.y[i].stream(a.y, m * a.ldy + piece(i) * 8);
-        if (a.h) r.h[i].stream(a.h, m * a.ldh + piece(i) * 8);
-      }
+      if (in[i] && a.y) y[i].stream(py + at[i] * 2);
+      if (in[i] && a.h) h[i].stream(ph + at[i] * kHb);
     }
   };
   griddep_launch_dependents();
   griddep_wait();
-  Row next;
-  if (kAhead) load_row(next, static_cast<int>(blockIdx.x));
-  for (int m = static_cast<int>(blockIdx.x); m < a.M; m += step) {
-    Row row;
-    if (kAhead) {
-      row = next;
-      if (m + step < a.M) load_row(next, m + step);
-    } else {
-      load_row(row, m);
-    }
-    float post = 1.0f;
+  load_row(static_cast<int>(blockIdx.x));
+  const float inv_d = 1.0f / static_cast<float>(D);
+  const uint64_t offset = both(a.offset), res = both(a.res_scale);
+#pragma unroll 1
+  for (int m = static_cast<int>(blockIdx.x); m < a.M; m += static_cast<int>(gridDim.x)) {
+    uint64_t post = both(1.0f);
     if (a.post_w) {
-      float ss = 0.0f;
+      uint64_t ss = 0;
 #pragma unroll
       for (int i = 0; i < kVec; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(row.y[i].at(j), row.y[i].at(j), ss);
-      post = rsqrtf(cta_sum(ss, part[0]) / static_cast<float>(D) + a.eps);
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t v = y[i].pair(j);
+          ss = f32x2_fma(v, v, ss);
+        }
+      post = both(rsqrtf(cta_sum(f32x2_sum(ss), part[0]) * inv_d + a.eps));
     }
-    const long long gate_at = static_cast<long long>(a.gate ? m / a.rows_per_gate : 0) * D;
-    float r[kVec][8];
-    float ss = 0.0f;
+    uint64_t r[kVec][4], ss = 0;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      if (piece(i) >= nvec) continue;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) r[i][j] = row.y[i].at(j);
+      for (int j = 0; j < 4; ++j) r[i][j] = y[i].pair(j);
+      if (!in[i]) continue;
       if (a.post_w) {
         Raw8<kWf32> w;
-        w.load(a.post_w, piece(i) * 8);
+        w.load(a.post_w, at[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] = r[i][j] * post * (w.at(j) + a.offset);
+        for (int j = 0; j < 4; ++j) r[i][j] = f32x2_mul(f32x2_mul(r[i][j], post), f32x2_add(w.pair(j), offset));
       }
-      if (a.gate && a.gate_f32) {
-        Raw8<true> g;
-        g.load(a.gate, gate_at + piece(i) * 8);
+      if (a.gate) {
+        const uint8_t* g = static_cast<const uint8_t*>(a.gate) +
+                           static_cast<long long>(m / a.rows_per_gate) * D * (a.gate_f32 ? 4 : 2);
+        if (a.gate_f32) {
+          Raw8<true> v;
+          v.load(g, at[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] *= g.at(j);
-      } else if (a.gate) {
-        Raw8<false> g;
-        g.load(a.gate, gate_at + piece(i) * 8);
+          for (int j = 0; j < 4; ++j) r[i][j] = f32x2_mul(r[i][j], v.pair(j));
+        } else {
+          Raw8<false> v;
+          v.load(g, at[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] *= g.at(j);
+          for (int j = 0; j < 4; ++j) r[i][j] = f32x2_mul(r[i][j], v.pair(j));
+        }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        r[i][j] = fmaf(a.res_scale, row.h[i].at(j), r[i][j]);
-        ss = fmaf(r[i][j], r[i][j], ss);
+      for (int j = 0; j < 4; ++j) {
+        r[i][j] = f32x2_fma(res, h[i].pair(j), r[i][j]);
+        ss = f32x2_fma(r[i][j], r[i][j], ss);
       }
       if (a.h_out) {
-        const long long at = m * a.ldho + piece(i) * 8;
+        uint8_t* p = static_cast<uint8_t*>(a.h_out) + (m * a.ldho + at[i]) * kHb;
         if (kHf32) {
-          float4* q = reinterpret_cast<float4*>(static_cast<float*>(a.h_out) + at);
-          q[0] = make_float4(r[i][0], r[i][1], r[i][2], r[i][3]);
-          q[1] = make_float4(r[i][4], r[i][5], r[i][6], r[i][7]);
+          ulonglong2* q = reinterpret_cast<ulonglong2*>(p);
+          q[0] = make_ulonglong2(r[i][0], r[i][1]);
+          q[1] = make_ulonglong2(r[i][2], r[i][3]);
         } else {
-          *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.h_out) + at) = to_bf16x8(r[i]);
+          *reinterpret_cast<uint4*>(p) =
+              make_uint4(pack_bf16(r[i][0]), pack_bf16(r[i][1]), pack_bf16(r[i][2]), pack_bf16(r[i][3]));
         }
       }
     }
+    if (m + static_cast<int>(gridDim.x) < a.M) load_row(m + static_cast<int>(gridDim.x));
     if (!a.pre_w) {
       if (a.post_w) __syncthreads();      // the one sum of this row is read before the next row's is written
       continue;
     }
-    const float s = rsqrtf(cta_sum(ss, part[1]) / static_cast<float>(D) + a.eps);
-    uint32_t top[kVec];
+    const uint64_t pre = both(rsqrtf(cta_sum(f32x2_sum(ss), part[1]) * inv_d + a.eps));
+    float top[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      const int c = piece(i);
-      top[i] = 0;
-      if (c < nvec) {
-        Raw8<kWf32> w;
-        w.load(a.pre_w, c * 8);
+      top[i] = 0.0f;
+      if (!in[i]) continue;
+      Raw8<kWf32> w;
+      w.load(a.pre_w, at[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          r[i][j] = r[i][j] * s * (w.at(j) + a.offset);
-          top[i] = max(top[i], __float_as_uint(r[i][j]) & 0x7FFFFFFFu);
-        }
-        if (a.x_out) *reinterpret_cast<uint4*>(a.x_out + static_cast<long long>(m) * D + c * 8) = to_bf16x8(r[i]);
+      for (int j = 0; j < 4; ++j) {
+        r[i][j] = f32x2_mul(f32x2_mul(r[i][j], pre), f32x2_add(w.pair(j), offset));
+        if (a.codes) top[i] = max_abs(top[i], r[i][j]);
       }
+      if (a.x_out)
+        *reinterpret_cast<uint4*>(a.x_out + static_cast<long long>(m) * D + at[i]) =
+            make_uint4(pack_bf16(r[i][0]), pack_bf16(r[i][1]), pack_bf16(r[i][2]), pack_bf16(r[i][3]));
     }
     if (a.codes) {
       // 16 lanes hold a block of 128 (a piece index is a multiple of 16 at every 16th lane);
-      // lane i of the 16 does the two divisions of piece i's block
+      // lane i of the 16 does the two divisions of piece i's block and stores its scale
       const int who = threadIdx.x & 15;
       uint32_t mine = 0;
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
+        uint32_t t = __float_as_uint(top[i]);        // not negative, NaN above all: ordered as integers
 #pragma unroll
-        for (int o = 8; o; o >>= 1) top[i] = max(top[i], __shfl_xor_sync(0xFFFFFFFFu, top[i], o));
-        if (who == i) mine = top[i];
+        for (int o = 8; o; o >>= 1) t = max(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
+        if (who == i) mine = t;
       }
-      const Fp8Scale f = fp8_block_scale(mine);
+      const Fp8Scale f = fp8_block_scale(mine & 0x7FFFFFFFu);
 #pragma unroll
       for (int i = 0; i < kVec; ++i) {
-        const int c = piece(i);
-        const float inv = __shfl_sync(0xFFFFFFFFu, f.inv, i, 16);
-        if (c >= nvec) continue;
-        *reinterpret_cast<uint2*>(a.codes + static_cast<long long>(m) * D + c * 8) =
-            make_uint2(e4m3x4_from_f32(__fmul_rn(r[i][0], inv), __fmul_rn(r[i][1], inv), __fmul_rn(r[i][2], inv),
-                                       __fmul_rn(r[i][3], inv)),
-                       e4m3x4_from_f32(__fmul_rn(r[i][4], inv), __fmul_rn(r[i][5], inv), __fmul_rn(r[i][6], inv),
-                                       __fmul_rn(r[i][7], inv)));
-      }
-      // lane i also stores that block's scale; its own piece i may lie past the row's end when the block does not
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        const int blk = piece(i) >> 4;
+        const uint64_t inv = both(__shfl_sync(0xFFFFFFFFu, f.inv, i, 16));
+        const int blk = at[i] >> 7;
         if (who == i && blk < (D + 127) / 128) a.scales[static_cast<size_t>(blk) * a.M + m] = f.scale;
+        if (!in[i]) continue;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) split(f32x2_mul(r[i][j], inv), v[2 * j], v[2 * j + 1]);
+        *reinterpret_cast<uint2*>(a.codes + static_cast<long long>(m) * D + at[i]) =
+            make_uint2(e4m3x4_from_f32(v[0], v[1], v[2], v[3]), e4m3x4_from_f32(v[4], v[5], v[6], v[7]));
       }
     }
     // With one sum per row, and a single barrier in it, a fast warp could write the next row's
@@ -221,9 +249,9 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
   }
 }
 
-template <int kVec, int kMaxThreads, bool kAhead, bool kHf32, bool kWf32>
+template <int kVec, int kMaxThreads, bool kHf32, bool kWf32>
 cudaError_t launch_one(const BlockNormArgs& a, cudaStream_t s) {
-  auto kernel = block_norm_kernel<kVec, kMaxThreads, kAhead, kHf32, kWf32>;
+  auto kernel = block_norm_kernel<kVec, kMaxThreads, kHf32, kWf32>;
   const int nvec = a.D / 8, warps = ((nvec + kVec - 1) / kVec + 31) / 32;
   // as many CTAs as run at once, at most one per row
   static std::atomic<int> per_sm[kMaxThreads / 32 + 1];
@@ -240,11 +268,10 @@ cudaError_t launch_one(const BlockNormArgs& a, cudaStream_t s) {
 template <bool kHf32, bool kWf32>
 cudaError_t launch_typed(const BlockNormArgs& a, cudaStream_t s) {
   // A few rows: one piece a thread, the shortest way through a row.  Many: two, so that
-  // several rows are under way on an SM (four with half the threads: 5% slower).  Above 8192
-  // columns the registers do not hold a second row.
-  if (a.D <= 2048 || (a.D <= 8192 && a.M <= num_sms())) return launch_one<1, 1024, true, kHf32, kWf32>(a, s);
-  if (a.D <= 8192) return launch_one<2, 512, true, kHf32, kWf32>(a, s);
-  return launch_one<4, 1024, false, kHf32, kWf32>(a, s);
+  // several rows are under way on an SM.
+  if (a.D <= 2048 || (a.D <= 8192 && a.M <= num_sms())) return launch_one<1, 1024, kHf32, kWf32>(a, s);
+  if (a.D <= 8192) return launch_one<2, 512, kHf32, kWf32>(a, s);
+  return launch_one<4, 1024, kHf32, kWf32>(a, s);
 }
 
 }  // namespace
