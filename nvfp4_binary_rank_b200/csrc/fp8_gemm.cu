@@ -159,13 +159,9 @@ struct Cfg {
   static constexpr uint32_t kTmemCols = kBufs * kBN;
   static constexpr int kTok = kSwap ? kBN : 128;               // token scales per block
   static constexpr int kRing = kStages + kBufs;                // blocks of scales (see the scale warp)
-  // rows form: registers of a promoting thread and of the others (setmaxnreg)
-  static constexpr int kRegLaunch = 96, kRegPromote = 104, kRegOther = 64;
-  static constexpr int kRegTotal = 128 * kGroups * kRegPromote + 128 * kRegOther;
   static constexpr int kPitch = kSwap ? 128 : kBN + 4;         // floats per row of the split-K exchange
   static_assert(kStages * kStageBytes >= (kSwap ? kBN : 128) * kPitch * 4, "the exchange reuses the stages");
   // a stage's "done" phase must be seen by the promoting warps before the next one ends
-  static_assert(kSwap || kRegTotal <= kThreads * kRegLaunch, "");
   static_assert(kBufs <= kStages && kTmemCols * kCtasPerSm <= 512, "");
 };
 
@@ -297,9 +293,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     record_error(&g_fp8_status, kDevErrTimeout);
   };
 
-  // Rows form: the promoting warps take registers from the others.
   if (warp < 4) {
-    if (!kSwap) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegOther));
     if (warp == 0) {
       if (elect_one()) {
         // ---- producer.  The weight tiles of the first stages are requested before the wait
@@ -460,10 +454,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       if (!ok) give_up();
     }
     __syncwarp();
-    if (!kSwap) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegLaunch));
   } else {
     // ---- promotion: one thread per MMA row and group of kCols columns
-    if (!kSwap) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegPromote));
     griddep_wait();
     const int grp = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     const int sub = kSwap ? 0 : grp >> 1;                     // rows form: this group's half of the tile
@@ -578,7 +570,6 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       }
     }
     __syncwarp();
-    if (!kSwap) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegLaunch));
   }
 
   // every role comes here, in the failing case too
@@ -642,15 +633,6 @@ cudaError_t launch_instance(const CUtensorMap& ta, const CUtensorMap& tb, Fp8Gem
   std::call_once(d.once, [&] {
     d.err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (d.err != cudaSuccess) return;
-    cudaFuncAttributes fa;
-    d.err = cudaFuncGetAttributes(&fa, kernel);
-    if (d.err != cudaSuccess) return;
-    // setmaxnreg hands out the registers that the block was launched with; with fewer of
-    // them the promoting warps would wait for ever
-    if (!kSwap && fa.numRegs * C::kThreads < C::kRegTotal) {
-      d.err = cudaErrorInvalidKernelImage;
-      return;
-    }
     for (int split = 1; split <= kMaxSplit; ++split) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(static_cast<unsigned>(split * C::kPair));

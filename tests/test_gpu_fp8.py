@@ -178,6 +178,20 @@ def test_gemm_rows_do_not_depend_on_the_batch_beside_them(nb):
     assert torch.equal(a, nb.fp8_gemm(xc, xs, wc, ws))
 
 
+def test_gemm_many_calls_in_a_row(nb):
+    """Thousands of launches back to back, of both forms and with K split and not: every block of
+    every launch has to come to an end by itself, whatever runs before and after it."""
+    sets = [operands(nb, np.random.default_rng(m), m, n, k) for m, n, k in ((333, 1000, 2064), (700, 640, 400), (3, 512, 1040))]
+    want = [nb.fp8_gemm(*s) for s in sets]
+    for i in range(3000):
+        j = i % 3 if i % 100 < 50 else 0
+        y = nb.fp8_gemm(*sets[j])
+        if i % 500 == 0:
+            assert torch.equal(y, want[j])
+    assert torch.equal(y, want[j])
+    assert nb.last_error() == 0
+
+
 def test_gemm_out_argument_and_neighbours_untouched(nb):
     M, N, K = 5, 100, 144
     xc, xs, wc, ws = operands(nb, np.random.default_rng(6), M, N, K)
