@@ -159,9 +159,14 @@ struct Cfg {
   static constexpr uint32_t kTmemCols = kBufs * kBN;
   static constexpr int kTok = kSwap ? kBN : 128;               // token scales per block
   static constexpr int kRing = kStages + kBufs;                // blocks of scales (see the scale warp)
+  // Rows form: registers of a promoting thread and of the others.  They are moved by
+  // setmaxnreg out of the block's launch allocation, which the three numbers have to fit.
+  static constexpr int kRegLaunch = 96, kRegPromote = 104, kRegOther = 64;
+  static constexpr int kRegTotal = 128 * kGroups * kRegPromote + 128 * kRegOther;
   static constexpr int kPitch = kSwap ? 128 : kBN + 4;         // floats per row of the split-K exchange
   static_assert(kStages * kStageBytes >= (kSwap ? kBN : 128) * kPitch * 4, "the exchange reuses the stages");
   // a stage's "done" phase must be seen by the promoting warps before the next one ends
+  static_assert(kSwap || kRegTotal <= kThreads * kRegLaunch, "");
   static_assert(kBufs <= kStages && kTmemCols * kCtasPerSm <= 512, "");
 };
 
@@ -293,7 +298,11 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     record_error(&g_fp8_status, kDevErrTimeout);
   };
 
+  // Rows form: the promoting warps take registers from the others.  Nobody takes any back
+  // before the barrier that ends all roles: a warp without work that did so at once left the
+  // promoting warps waiting for registers, and the block with them.
   if (warp < 4) {
+    if (!kSwap) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegOther));
     if (warp == 0) {
       if (elect_one()) {
         // ---- producer.  The weight tiles of the first stages are requested before the wait
@@ -456,6 +465,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     __syncwarp();
   } else {
     // ---- promotion: one thread per MMA row and group of kCols columns
+    if (!kSwap) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegPromote));
     griddep_wait();
     const int grp = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
     const int sub = kSwap ? 0 : grp >> 1;                     // rows form: this group's half of the tile
@@ -570,10 +580,15 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       }
     }
     __syncwarp();
+    if (!kSwap) {
+      named_barrier(1, 128 * C::kGroups);      // between two setmaxnreg of a warpgroup
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::kRegLaunch));
+    }
   }
 
   // every role comes here, in the failing case too
   __syncthreads();
+  if (!kSwap && warp < 4) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::kRegLaunch));
   if (p.split > 1) {
     cluster_sync_all();
     // output rows of the exchange: tokens; this CTA finishes rows part, part + split, ...
@@ -633,6 +648,14 @@ cudaError_t launch_instance(const CUtensorMap& ta, const CUtensorMap& tb, Fp8Gem
   std::call_once(d.once, [&] {
     d.err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (d.err != cudaSuccess) return;
+    cudaFuncAttributes fa;
+    d.err = cudaFuncGetAttributes(&fa, kernel);
+    if (d.err != cudaSuccess) return;
+    // with fewer registers at launch than are handed out the promoting warps would wait for ever
+    if (!kSwap && fa.numRegs * C::kThreads < C::kRegTotal) {
+      d.err = cudaErrorInvalidKernelImage;
+      return;
+    }
     for (int split = 1; split <= kMaxSplit; ++split) {
       cudaLaunchConfig_t cfg = {};
       cfg.gridDim = dim3(static_cast<unsigned>(split * C::kPair));
