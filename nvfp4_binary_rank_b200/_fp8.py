@@ -3,8 +3,11 @@
 Argument checks and marshalling only.  Outputs are allocated on the stream the call
 runs on, and the call runs on its tensors' device whatever the current one is.
 
-A decode step calls these once per layer with microseconds of GPU work, so the checks of
-a good call are attribute reads in line; only a bad one is looked at closely, by _refuse.
+A decode step calls these once per layer with microseconds of GPU work, so a plain call
+(contiguous operands, the current device and stream) goes through _binding.so, which checks
+it, allocates its outputs and calls the library.  What that does not take comes back as None
+and is checked here: strided rows, another stream or device, an output to write into, and
+every call that is refused.
 """
 
 from __future__ import annotations
@@ -20,6 +23,27 @@ _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
 _empty = torch.empty
 _SCORE = {"softmax": 0, "sigmoid": 1}
+_fast = None
+
+
+def _load_fast():
+    """The fast path's module (loads the library first: it links to it)."""
+    global _fast
+    _lib.load()
+    try:
+        from . import _binding
+    except ImportError as e:
+        raise RuntimeError("_binding.so is missing or does not fit this PyTorch: build it with "
+                           "`python -m nvfp4_binary_rank_b200.build`") from e
+    _fast = _binding
+    return _binding
+
+
+def _done(r, fn: str):
+    """A fast call's outputs; its status, if it is one, raised."""
+    if r.__class__ is int:
+        _check(fn, r)
+    return r
 
 
 def _refuse(dev: int, *operands):
@@ -63,6 +87,10 @@ def _rows_ok(t, dtype, dev) -> bool:
 def fp8_quant_act(x: torch.Tensor, stream=None):
     """BF16 [M, K] (rows contiguous, any row stride that is a multiple of 8) ->
     (codes float8_e4m3fn [M, K], scales float32 [ceil(K/128), M])."""
+    if stream is None:
+        r = (_fast or _load_fast()).quant_act(x)
+        if r is not None:
+            return _done(r, "biloco_fp8_quant_act")
     dev = x.get_device() if isinstance(x, torch.Tensor) else -1
     if dev < 0 or not _rows_ok(x, _BF16, dev):
         _refuse(dev, (x, "x", (_BF16,), (None, None), False))
@@ -100,6 +128,11 @@ def fp8_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.Tenso
              out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """y[m, n] = sum_b x_scales[b, m] w_scales[n/128, b] (x[m] . w[n])_b over blocks b of 128
     along K, for any number of rows; y is bfloat16 or float32."""
+    if stream is None and (out is not None or out_dtype in _TYPE):
+        r = (_fast or _load_fast()).gemm(x_codes, x_scales, w_codes, w_scales, out,
+                                         (out_dtype if out is None else getattr(out, "dtype", None)) is _F32)
+        if r is not None:
+            return _done(r, "biloco_fp8_gemm")
     try:
         dev = x_codes.get_device()
         M, K = x_codes.shape
@@ -154,6 +187,10 @@ def block_norm(y: torch.Tensor | None, h: torch.Tensor | None, *, post_weight: t
     (each row serves M / G consecutive rows).  Returns (h', x), (h', codes, scales) with
     `quant` (as fp8_quant_act lays them out), or h' alone without pre_weight.  out_h may
     be h itself."""
+    if stream is None and out_h is None:
+        r = (_fast or _load_fast()).norm(y, h, post_weight, pre_weight, gate, res_scale, offset, eps, bool(quant))
+        if r is not None:
+            return _done(r, "biloco_block_norm")
     ref = h if y is None else y
     if ref is None:
         raise ValueError("y or h must be given")
@@ -236,6 +273,11 @@ def fp8_moe(x: torch.Tensor, router: torch.Tensor, w13: torch.Tensor, w13_scales
     shared: they serve every token with weight 1.  `score` is "softmax" (over the experts)
     or "sigmoid"; bias float32 [E] is added for the choice only.  Returns (y bfloat16
     [T, D], ids int32 [T, top_k], weights float32 [T, top_k])."""
+    if stream is None and score in _SCORE:
+        r = (_fast or _load_fast()).moe(x, router, w13, w13_scales, w2, w2_scales, bias, top_k, _SCORE[score], bool(renorm),
+                                        route_scale)
+        if r is not None:
+            return _done(r, "biloco_fp8_moe")
     for t, name, nd in ((x, "x", 2), (router, "router", 2), (w13, "w13", 3)):
         if not isinstance(t, torch.Tensor) or t.dim() != nd:
             raise ValueError(f"{name} must be a {nd}-D CUDA tensor")

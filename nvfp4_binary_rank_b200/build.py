@@ -1,4 +1,4 @@
-"""Build libbiloco.so (sm_100a) in-tree with nvcc.
+"""Build libbiloco.so (sm_100a) in-tree with nvcc, and the Python fast path beside it.
 
     python -m nvfp4_binary_rank_b200.build          # incremental
     python -m nvfp4_binary_rank_b200.build --force  # rebuild
@@ -24,6 +24,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libbiloco.so")
+BINDING = os.path.join(PKG, "_binding.so")
 OBJ = os.path.join(PKG, "_build")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -67,7 +68,40 @@ def _compile(src, force, verbose):
     return obj
 
 
+def _build_binding(force, verbose):
+    """The FP8 operators' fast Python path (csrc/binding.cpp), against PyTorch's headers."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    src = os.path.join(CSRC, "binding.cpp")
+    newest = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "biloco.h"), torch.__file__))
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+        return
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-I{p}" for p in [*cpp_extension.include_paths(), cuda, sysconfig.get_paths()["include"]]),
+           src, "-o", BINDING + ".tmp", f"-L{PKG}", "-l:libbiloco.so", "-Wl,-rpath,$ORIGIN",
+           *(f"-L{p}" for p in cpp_extension.library_paths()), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
+           "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+        raise RuntimeError("the compiler failed on binding.cpp")
+    os.replace(BINDING + ".tmp", BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    lib = _build_library(force, verbose)
+    _build_binding(force, verbose)
+    return lib
+
+
+def _build_library(force, verbose) -> str:
     os.makedirs(OBJ, exist_ok=True)
     srcs = sources()
     with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
