@@ -425,10 +425,14 @@ __device__ __forceinline__ void scale_hidden(uint32_t (&v)[8], int2 e, int row_e
 // megabytes at a time: with a run of items of its own for each CTA, 1.4 GB of experts took
 // twice as long (the pages of 296 places do not fit the address caches).  More than 16 tokens
 // of an expert take further passes over the item's weights, which then come from L2.
-template <bool kUp>
+//
+// kOne (down, one token): a cluster of the token's experts owns 64 output rows; the shares meet
+// in distributed shared memory and there is no combine kernel.
+template <bool kUp, int kSplit, bool kOne = false>
 __global__ void __launch_bounds__(kThreads, 2)
 moe_product_kernel(const __grid_constant__ MoeArgs a) {
-  constexpr int kSplit = kUp ? 8 : 4, kGroups = kWarps / kSplit;
+  constexpr int kGroups = kWarps / kSplit;
+  __shared__ float own[kOne ? 32 * kGroups : 1];
   extern __shared__ __align__(16) uint8_t stream[];
   __shared__ Lists l;
   __shared__ float4 red[2][kWarps][kTiles][32];
@@ -440,7 +444,9 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
   const int K = kUp ? a.D : a.F, F = a.F, D = a.D, KT = a.k + a.shared;
   const int KB = (K + 127) / 128, NB = ((kUp ? 2 * F : D) + 127) / 128;
   const int groups = kUp ? F / 16 : (D + 31) / 32, per = (groups + kGroups - 1) / kGroups;   // items of an expert
-  const int items = l.nact * per, stride = static_cast<int>(gridDim.x);
+  const int items = l.nact * per, stride = kOne ? items : static_cast<int>(gridDim.x);
+  const int first = kOne ? static_cast<int>(cta_rank()) * per + static_cast<int>(blockIdx.x) / (a.k + a.shared)
+                         : static_cast<int>(blockIdx.x);
   const int sub = warp / kSplit, kp = warp % kSplit;
   const int b0 = KB * kp / kSplit, b1 = KB * (kp + 1) / kSplit, runs = 2 * (b1 - b0);
   const uint8_t* const W = kUp ? a.w13 : a.w2;
@@ -448,7 +454,7 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
 
   // ---- the weight stream
   const uint32_t ring = smem_u32(stream) + warp * (kStages * kRunBytes) + lane * 16;
-  int ci = static_cast<int>(blockIdx.x), cp = 0, cr = 0, cslot = 0, ccount = 0;
+  int ci = first, cp = 0, cr = 0, cslot = 0, ccount = 0;
   const uint8_t* cbase = nullptr;
   int o1 = 8 * K, o2 = kUp ? F * K : 16 * K, o3 = o2 + 8 * K;      // offsets of tiles 1 to 3
   auto seek = [&] {
@@ -496,82 +502,75 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
     constexpr bool kWide = decltype(wide_t)::value;
     constexpr int kHalves = kWide ? 2 : 1;
     // this lane's token of either eight, as the products' second operand
-    const uint16_t* px[2];
-    const int2* pe[2];
+    int row[2], rexp[2];
     bool has[2];
-    int rexp[2];
 #pragma unroll
     for (int h = 0; h < kHalves; ++h) {
       has[h] = h * 8 + g < cnt;
       const int q = has[h] ? pairs[h * 8 + g] : 0;
-      const long long r = kUp ? q / KT : q;
-      px[h] = A + r * K + b0 * 128 + t4 * 16;
-      if (!kUp) {
-        pe[h] = reinterpret_cast<const int2*>(a.hexp + r * (F / 8)) + (b0 * 8 + t4);
-        rexp[h] = exponent_of(__ldcg(a.hmax + q));
-      }
+      row[h] = kUp ? q / KT : q;
+      if (!kUp) rexp[h] = exponent_of(__ldcg(a.hmax + q));
     }
     const int n = min(grp0 + sub, groups - 1) * (kUp ? 16 : 32);
     const float* S = (kUp ? a.s13 : a.s2) + (static_cast<long long>(e) * NB + n / 128) * KB;
-    const float* S2 = kUp ? a.s13 + (static_cast<long long>(e) * NB + (F + n) / 128) * KB : S;
+    const int up_rows = kUp ? ((F + n) / 128 - n / 128) * KB : 0;      // from the gate's scales to the up rows'
     float out[2][2][4];
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
 #pragma unroll
       for (int i = 0; i < 2; ++i) out[h][i][0] = out[h][i][1] = out[h][i][2] = out[h][i][3] = 0.0f;
-    // Activations of a block: two runs of the first eight tokens a block ahead, of the others
-    // when they are needed.
-    struct Acts {
-      uint32_t x[2][8];
-      int2 e[2];
-      float s, s2;
-    };
-    auto clear = [](uint32_t (&v)[8]) {
+    // activations, a run ahead of the products
+    uint32_t x[2][2][8];
+    int2 xe[2][2];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0;
-    };
-    Acts even, odd;
-    clear(even.x[0]);
-    clear(even.x[1]);
-    clear(odd.x[0]);
-    clear(odd.x[1]);
-    even.e[0] = even.e[1] = odd.e[0] = odd.e[1] = make_int2(0, 0);
-    auto fetch = [&](Acts& f, int b) {
-      const bool tail = b + 1 == KB && (K & 127);     // the last block may end anywhere
-      f.s = __ldg(S + b);
-      f.s2 = kUp ? __ldg(S2 + b) : 0.0f;
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int r = 2 * (b - b0) + c;
-        const bool in = !tail || b * 128 + c * 64 + t4 * 16 < K;
-        if (tail) clear(f.x[c]);
-        load_run(f.x[c], px[0] + r * 64, has[0] && in);
-        if (!kUp && has[0] && in) f.e[c] = __ldcg(pe[0] + r * 4);
+      for (int h = 0; h < 2; ++h) {
+        xe[c][h] = make_int2(0, 0);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[c][h][j] = 0;
+      }
+    auto fetch = [&](uint32_t (&v)[2][8], int2 (&ve)[2], int r) {
+      const int k = b0 * 128 + r * 64 + t4 * 16;
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h) {
+        if (K & 127) {                                // the last block may end anywhere
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[h][j] = 0;
+        }
+        const bool in = has[h] && k < K;
+        load_run(v[h], A + static_cast<long long>(row[h]) * K + k, in);
+        if (!kUp && in) ve[h] = __ldcg(reinterpret_cast<const int2*>(a.hexp + (static_cast<long long>(row[h]) * F + k) / 8));
       }
     };
-    auto block = [&](Acts& cur, Acts& next, int b) {
-      uint32_t y[8];
+    float s_gate = 0.0f, s_up = 0.0f;
+    if (runs) {
+      fetch(x[0], xe[0], 0);
+      s_gate = __ldg(S + b0);
+      s_up = __ldg(S + b0 + up_rows);
+    }
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+      const float s0 = s_gate, s1 = s_up;
       float k0[2][4], k1[2][4];
-      if (kWide) clear(y);
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) k0[i][j] = k1[i][j] = 0.0f;
-      if (b + 1 < b1) fetch(next, b + 1);
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        if (kWide) {
-          const int r = 2 * (b - b0) + c;
-          const bool in = b * 128 + c * 64 + t4 * 16 < K;
-          if (c == 1 && !in) clear(y);
-          int2 ye = make_int2(0, 0);
-          load_run(y, px[1] + r * 64, has[1] && in);
-          if (!kUp && has[1] && in) ye = __ldcg(pe[1] + r * 4);
-          if (!kUp) scale_hidden(y, ye, rexp[1]);
+        const int r = 2 * (b - b0) + c;
+        if (c == 0 || b + 1 < b1) fetch(x[1 - c], xe[1 - c], r + 1);
+        if (c == 1 && b + 1 < b1) {
+          s_gate = __ldg(S + b + 1);
+          s_up = __ldg(S + b + 1 + up_rows);
         }
-        if (!kUp) scale_hidden(cur.x[c], cur.e[c], rexp[0]);
+        if (!kUp) {
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) scale_hidden(x[c][h], xe[c][h], rexp[h]);
+        }
         cp_async_wait<kStages - 2>();
-        mma_run<kWide>(k0, k1, ring + slot * kRunBytes, cur.x[c], y);
+        mma_run<kWide>(k0, k1, ring + slot * kRunBytes, x[c][0], x[c][1]);
         copy_run();                       // into the slot before this one, read by now
         slot = slot + 1 == kStages ? 0 : slot + 1;
       }
@@ -579,15 +578,9 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          out[0][i][j] = fmaf(k0[i][j], kUp && i ? cur.s2 : cur.s, out[0][i][j]);
-          if (kWide) out[1][i][j] = fmaf(k1[i][j], kUp && i ? cur.s2 : cur.s, out[1][i][j]);
+          out[0][i][j] = fmaf(k0[i][j], i ? s1 : s0, out[0][i][j]);
+          if (kWide) out[1][i][j] = fmaf(k1[i][j], i ? s1 : s0, out[1][i][j]);
         }
-    };
-    if (runs) fetch(even, b0);
-#pragma unroll 1
-    for (int b = b0; b < b1; b += 2) {
-      block(even, odd, b);
-      if (b + 1 < b1) block(odd, even, b + 1);
     }
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
@@ -596,13 +589,13 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
         sums[warp][h * 2 + i][lane] = make_float4(out[h][i][0], out[h][i][1], out[h][i][2], out[h][i][3]);
     __syncthreads();
     if (kUp) {
-      // a warp (in turn) for each eight tokens: product 0 are the gate rows, product 1 the up rows
-      const int h = (warp - 2 * step) & (kWarps - 1);
-      if (h < kHalves) {
+      // a warp (in turn) for each group and eight tokens: product 0 are the gate rows, product 1 the up rows
+      const int task = (warp - 2 * kGroups * step) & (kWarps - 1), grp = task >> 1, h = task & 1;
+      if (grp < kGroups && h < kHalves && grp0 + grp < groups) {
         float gs[4] = {0, 0, 0, 0}, us[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < kSplit; ++w) {
-          const float4 p = sums[w][2 * h][lane], q = sums[w][2 * h + 1][lane];
+          const float4 p = sums[grp * kSplit + w][2 * h][lane], q = sums[grp * kSplit + w][2 * h + 1][lane];
           gs[0] += p.x; gs[1] += p.y; gs[2] += p.z; gs[3] += p.w;
           us[0] += q.x; us[1] += q.y; us[2] += q.z; us[3] += q.w;
         }
@@ -612,13 +605,13 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
           const float xs = r < cnt ? a.xscale[q / KT] : 0.0f;
           int top = 0;
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {                 // hidden columns n + g and n + 8 + g
+          for (int i = 0; i < 2; ++i) {                 // hidden columns f + g, for each eight of the group's 16
             const float gv = gs[2 * i + j] * xs, uv = us[2 * i + j] * xs;
             const float v = gv / (1.0f + expf(-gv)) * uv;
             int m = static_cast<int>(__float_as_uint(v) & 0x7FFFFFFFu);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-            const int ex = exponent_of(m), f = n + i * 8;
+            const int ex = exponent_of(m), f = (grp0 + grp) * 16 + i * 8;
             top = max(top, m);
             if (r < cnt) {
               a.h[static_cast<long long>(q) * F + f + g] = static_cast<uint16_t>(f16x2_from_f32(v * pow2(-ex), 0.0f));
@@ -629,13 +622,15 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
         }
       }
     } else {
-      // warp (group, eight tokens, product): the sums of the group's kSplit warps
-      const int h = (warp >> 1) & 1, i = warp & 1, row = (grp0 + warp / 4) * 32 + i * 16 + g;
-      if (h < kHalves) {
+      // task (group, eight tokens, product): the sums of the group's kSplit warps
+#pragma unroll
+      for (int task = warp; task < 4 * kGroups; task += kWarps) {
+        const int grp = task >> 2, h = (task >> 1) & 1, i = task & 1, row = (grp0 + grp) * 32 + i * 16 + g;
+        if (h >= kHalves) continue;
         float v[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < kSplit; ++w) {
-          const float4 p = sums[warp / 4 * kSplit + w][h * 2 + i][lane];
+          const float4 p = sums[grp * kSplit + w][h * 2 + i][lane];
           v[0] += p.x; v[1] += p.y; v[2] += p.z; v[3] += p.w;
         }
 #pragma unroll
@@ -644,15 +639,20 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
           if (r < cnt) {
             const int q = pairs[r];
             const float w = __ldcg(a.pair_w + q) * pow2(exponent_of(__ldcg(a.hmax + q)) - 14);
-            float* y = a.share + static_cast<long long>(q) * D + row;
-            if (row < D) y[0] = w * v[j];
-            if (row + 8 < D) y[8] = w * v[2 + j];
+            if (kOne) {
+              own[grp * 32 + i * 16 + g] = w * v[j];
+              own[grp * 32 + i * 16 + g + 8] = w * v[2 + j];
+            } else {
+              float* y = a.share + static_cast<long long>(q) * D + row;
+              if (row < D) y[0] = w * v[j];
+              if (row + 8 < D) y[8] = w * v[2 + j];
+            }
           }
         }
       }
     }
   };
-  for (int it = static_cast<int>(blockIdx.x), p0 = 0, step = 0; it < items; ++step) {
+  for (int it = first, p0 = 0, step = 0; it < items; ++step) {
     const int act = it / per, e = l.active[act], grp0 = (it - act * per) * kGroups;
     const int cnt = min(16, l.count[e] - p0);
     const int* pairs = l.pairs + l.begin[e] + p0;
@@ -662,6 +662,22 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
     else pass(std::false_type(), e, grp0, pairs, cnt, red[step & 1], step);
     p0 = more ? p0 + 16 : 0;
     if (!more) it += stride;
+  }
+  if (kOne) {
+    cluster_barrier();
+    const int row = (first % per) * 32 * kGroups + tid;
+    if (cta_rank() == 0 && tid < 32 * kGroups && row < D) {
+      const uint32_t at = smem_u32(own + tid);
+      float v[8], sum = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < KT) asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[j]) : "r"(mapa_u32(at, j)));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < KT) sum += v[j];
+      a.y[row] = static_cast<uint16_t>(bf16x2_from_f32(sum, 0.0f));
+    }
+    cluster_barrier();             // the first CTA may still be reading this one's sums
   }
 }
 
@@ -694,6 +710,34 @@ struct MoeSetup {
   std::once_flag once;
   cudaError_t err = cudaSuccess;
 };
+
+// How many warps share a row group's K.  With few, an item is larger and its barrier and
+// joining cost less per byte; with many, the items deal out more evenly over the CTAs.  Both
+// sides in units of a warp's time for one block of 128: rounds of items times a warp's
+// blocks plus about 1.5 for the end of an item.  Measured, us of the up and the down kernel
+// at 64 tokens, 65 experts of 3 x 5120 x 2048: UPDOWN.
+template <bool kUp>
+cudaError_t launch_product(const MoeArgs& a, int experts, cudaStream_t s) {
+  const long long slots = 2LL * num_sms();
+  const int KB = ((kUp ? a.D : a.F) + 127) / 128, groups = kUp ? a.F / 16 : (a.D + 31) / 32;
+  int best = 8;
+  double cost = 0.0;
+  long long best_items = 0;
+  for (int split = 8; split >= 2; split /= 2) {
+    const int per = (groups + kWarps / split - 1) / (kWarps / split);
+    const long long items = static_cast<long long>(experts) * per;
+    const double c = static_cast<double>((items + slots - 1) / slots) * ((KB + split - 1) / split + 1.5);
+    if (split == 8 || c < cost) {
+      best = split;
+      cost = c;
+      best_items = items;
+    }
+  }
+  const unsigned grid = static_cast<unsigned>(std::min(slots, best_items));
+  if (best == 8) return launch_pdl(moe_product_kernel<kUp, 8>, grid, kThreads, kStreamBytes, 1, s, a);
+  if (best == 4) return launch_pdl(moe_product_kernel<kUp, 4>, grid, kThreads, kStreamBytes, 1, s, a);
+  return launch_pdl(moe_product_kernel<kUp, 2>, grid, kThreads, kStreamBytes, 1, s, a);
+}
 
 }  // namespace
 
@@ -730,8 +774,13 @@ cudaError_t launch_fp8_moe(MoeArgs& a, cudaStream_t s) {
     raise(moe_route_kernel<1, true>, BILOCO_MOE_MAX_D * 2);
     raise(moe_route_kernel<4, false>, 4 * BILOCO_MOE_MAX_D * 2);
     raise(moe_route_kernel<4, true>, 4 * BILOCO_MOE_MAX_D * 2);
-    raise(moe_product_kernel<true>, kStreamBytes);
-    raise(moe_product_kernel<false>, kStreamBytes);
+    raise(moe_product_kernel<true, 8>, kStreamBytes);
+    raise(moe_product_kernel<true, 4>, kStreamBytes);
+    raise(moe_product_kernel<true, 2>, kStreamBytes);
+    raise(moe_product_kernel<false, 8>, kStreamBytes);
+    raise(moe_product_kernel<false, 4>, kStreamBytes);
+    raise(moe_product_kernel<false, 2>, kStreamBytes);
+    raise(moe_product_kernel<false, 4, true>, kStreamBytes);
   });
   if (d.err != cudaSuccess) return d.err;
 
@@ -747,15 +796,15 @@ cudaError_t launch_fp8_moe(MoeArgs& a, cudaStream_t s) {
                      : launch_pdl(moe_route_kernel<4, false>, grid, kThreads, sm, kRouteCtas, s, a);
   if (e != cudaSuccess) return e;
 
-  const int slots = 2 * num_sms();
-  const int experts = min(a.T * a.k, a.E) + a.shared;
-  const long long up = static_cast<long long>(experts) * (a.F / 16);
-  e = launch_pdl(moe_product_kernel<true>, static_cast<unsigned>(std::min<long long>(slots, up)), kThreads, kStreamBytes, 1,
-                 s, a);
+  const int experts = std::min(a.T * a.k, a.E) + a.shared;
+  e = launch_product<true>(a, experts, s);
   if (e != cudaSuccess) return e;
-  const long long down = static_cast<long long>(experts) * ((a.D + 63) / 64);
-  e = launch_pdl(moe_product_kernel<false>, static_cast<unsigned>(std::min<long long>(slots, down)), kThreads, kStreamBytes,
-                 1, s, a);
+  if (a.T == 1 && a.k + a.shared <= 8) {
+    const unsigned n = static_cast<unsigned>(a.k + a.shared);
+    return launch_pdl(moe_product_kernel<false, 4, true>, static_cast<unsigned>((a.D + 63) / 64) * n, kThreads, kStreamBytes, n,
+                      s, a);
+  }
+  e = launch_product<false>(a, experts, s);
   if (e != cudaSuccess) return e;
   return launch_pdl(moe_combine_kernel, static_cast<unsigned>((a.T * (a.D / 4) + kThreads - 1) / kThreads), kThreads, 0, 1,
                     s, a);
