@@ -46,7 +46,6 @@ namespace {
 constexpr int kThreads = 256, kWarps = 8;
 constexpr int kTiles = 4;                 // 8-row weight tiles of one item
 constexpr int kRouteCtas = 8;             // cluster of the route kernel
-constexpr int kAhead = 5;                 // router pieces of 256 columns a lane has in flight
 
 __device__ __forceinline__ uint32_t mapa_u32(uint32_t addr, uint32_t rank) {
   uint32_t r;
@@ -85,23 +84,24 @@ __device__ __forceinline__ int exponent_of(uint32_t bits) {
 
 // ------------------------------------------------------------------ route
 
+// Eight router values as they lie in memory.
 template <bool kF32>
-__device__ __forceinline__ void load_router8(const void* p, long long at, float (&v)[8]) {
-  if (kF32) {
-    const float4* q = reinterpret_cast<const float4*>(static_cast<const float*>(p) + at);
-    const float4 a = __ldg(q), b = __ldg(q + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  } else {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + at));
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = bf16_lo(w[j]);
-      v[2 * j + 1] = bf16_hi(w[j]);
-    }
+struct RouterPiece {
+  uint4 q[kF32 ? 2 : 1];
+  __device__ __forceinline__ void load(const void* p, long long at, bool in) {
+    const uint4* s = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + at * (kF32 ? 4 : 2));
+    q[0] = in ? __ldg(s) : make_uint4(0, 0, 0, 0);
+    if (kF32) q[kF32] = in ? __ldg(s + 1) : make_uint4(0, 0, 0, 0);
   }
-}
+  __device__ __forceinline__ float lo(int i) const {          // value 2 i
+    if (kF32) return __uint_as_float((i & 1) ? q[kF32 ? i >> 1 : 0].z : q[kF32 ? i >> 1 : 0].x);
+    return bf16_lo(i == 0 ? q[0].x : i == 1 ? q[0].y : i == 2 ? q[0].z : q[0].w);
+  }
+  __device__ __forceinline__ float hi(int i) const {          // value 2 i + 1
+    if (kF32) return __uint_as_float((i & 1) ? q[kF32 ? i >> 1 : 0].w : q[kF32 ? i >> 1 : 0].y);
+    return bf16_hi(i == 0 ? q[0].x : i == 1 ? q[0].y : i == 2 ? q[0].z : q[0].w);
+  }
+};
 
 // Order-preserving integer key of a score: larger is better, 0 stands for "taken".  A score
 // that is no number gets 1, below every number.
@@ -116,18 +116,28 @@ __device__ __forceinline__ unsigned long long order_key(double v) {
 // rolled: one launch of a few CTAs pays for every instruction line it fetches (with the
 // selection unrolled over 512 experts the kernel took 18 us, mostly instruction misses).
 template <int kTok, bool kF32>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 1)
 moe_route_kernel(const __grid_constant__ MoeArgs a) {
   extern __shared__ __align__(16) uint8_t rows[];                       // [kTok][D] bf16
   __shared__ double score[kTok][kMoeMaxExperts];                        // the scores, then the weights
   __shared__ unsigned long long key[kTok][kMoeMaxExperts];
   __shared__ uint32_t part[kTok][kWarps];
   griddep_launch_dependents();
-  griddep_wait();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = static_cast<int>(cta_rank());
   const int t0 = static_cast<int>(blockIdx.x) / kRouteCtas * kTok;
   const int D = a.D, nvec = D / 8, ntok = min(kTok, a.T - t0);
+  // the router does not depend on the kernel before this one: the first loads of this warp's
+  // first expert are under way while that one ends
+  constexpr int kAhead = kF32 ? 5 : 10;               // pieces of 256 columns a lane has in flight
+  RouterPiece<kF32> w[kAhead];
+  auto load_pieces = [&](int e, int c0) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      w[u].load(a.router, static_cast<long long>(e) * D + (c0 + 32 * u) * 8, e < a.E && c0 + 32 * u < nvec);
+  };
+  load_pieces(rank + kRouteCtas * warp, lane);
+  griddep_wait();
   uint4* const xs = reinterpret_cast<uint4*>(rows);
 
   // the token rows into shared memory, and each row's largest magnitude
@@ -158,23 +168,17 @@ moe_route_kernel(const __grid_constant__ MoeArgs a) {
     for (int j = 0; j < kTok; ++j) s[j] = comp[j] = 0.0f;
 #pragma unroll 1
     for (int c0 = lane; c0 < nvec; c0 += 32 * kAhead) {
-      float w[kAhead][8];                             // the loads of kAhead pieces in flight
+      if (c0 != lane || e != rank + kRouteCtas * warp) load_pieces(e, c0);
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) w[u][i] = 0.0f;
-        if (c0 + 32 * u < nvec) load_router8<kF32>(a.router, static_cast<long long>(e) * D + (c0 + 32 * u) * 8, w[u]);
-      }
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
+        if (c0 + 32 * u >= nvec) break;
 #pragma unroll
         for (int j = 0; j < kTok; ++j) {
-          const uint4 q = xs[j * nvec + min(c0 + 32 * u, nvec - 1)];
+          const uint4 q = xs[j * nvec + c0 + 32 * u];
           const uint32_t v[4] = {q.x, q.y, q.z, q.w};
           float p = 0.0f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) p = fmaf(bf16_hi(v[i]), w[u][2 * i + 1], fmaf(bf16_lo(v[i]), w[u][2 * i], p));
-          if (c0 + 32 * u >= nvec) p = 0.0f;
+          for (int i = 0; i < 4; ++i) p = fmaf(bf16_hi(v[i]), w[u].hi(i), fmaf(bf16_lo(v[i]), w[u].lo(i), p));
           const float y = p - comp[j], t = s[j] + y;
           comp[j] = (t - s[j]) - y;
           s[j] = t;
@@ -712,10 +716,11 @@ struct MoeSetup {
 };
 
 // How many warps share a row group's K.  With few, an item is larger and its barrier and
-// joining cost less per byte; with many, the items deal out more evenly over the CTAs.  Both
-// sides in units of a warp's time for one block of 128: rounds of items times a warp's
-// blocks plus about 1.5 for the end of an item.  Measured, us of the up and the down kernel
-// at 64 tokens, 65 experts of 3 x 5120 x 2048: UPDOWN.
+// joining cost less per byte; with many, the items deal out more evenly over the CTAs.  The
+// estimate, in units of a warp's time for one block of 128: a warp's blocks plus 1.5 for the
+// end of an item, times the rounds of items plus 1.5.  Measured, us of a layer of 64 tokens and
+// 65 experts with 8, 4, 2 warps in the up kernel: 474, 461, 497 (3 x 5120 x 2048), 181, 197,
+// 225 (3 x 5120 x 512); in the down kernel 497, 474, 476 and 218, 181, 178.
 template <bool kUp>
 cudaError_t launch_product(const MoeArgs& a, int experts, cudaStream_t s) {
   const long long slots = 2LL * num_sms();
@@ -726,7 +731,7 @@ cudaError_t launch_product(const MoeArgs& a, int experts, cudaStream_t s) {
   for (int split = 8; split >= 2; split /= 2) {
     const int per = (groups + kWarps / split - 1) / (kWarps / split);
     const long long items = static_cast<long long>(experts) * per;
-    const double c = static_cast<double>((items + slots - 1) / slots) * ((KB + split - 1) / split + 1.5);
+    const double c = ((items + slots - 1) / slots + 1.5) * ((KB + split - 1) / split + 1.5);
     if (split == 8 || c < cost) {
       best = split;
       cost = c;
