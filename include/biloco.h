@@ -281,7 +281,7 @@ enum { BILOCO_TYPE_BF16 = 0, BILOCO_TYPE_F32 = 1 };
 /*
  * biloco_fp8_quant_act - BF16 activation -> FP8 blocks.
  *   x_bf16  [M][K] bfloat16, row stride ldx elements, 16-byte aligned; ldx % 8 == 0
- *   M, K    M >= 0 (0: nothing is done), K >= 16, K % 16 == 0
+ *   M, K    0 <= M <= 2^30 (0: nothing is done), K >= 16, K % 16 == 0, M ceil(K/512) < 2^31
  *   codes   out [M][K] E4M3 bytes, 16-byte aligned
  *   scales  out [ceil(K/128)][M] float (block-major: one token's scales are M apart)
  */
@@ -331,7 +331,7 @@ int biloco_fp8_gemm(const uint8_t *x_codes, const float *x_scales, const uint8_t
  *   x_bf16       out [M][D] bfloat16, or NULL
  *   codes,scales out x as FP8 blocks (D % 16 == 0), layout of biloco_fp8_quant_act, or NULL
  * h' enters x unrounded, and x the FP8 blocks unrounded: each output is rounded once.
- * limits: M >= 0, 8 <= D <= BILOCO_NORM_MAX_D, D % 8 == 0, row strides >= D and multiples of 8
+ * limits: 0 <= M <= 2^30, 8 <= D <= BILOCO_NORM_MAX_D, D % 8 == 0, row strides >= D and multiples of 8
  * elements, 16-byte aligned arrays.  Outputs must not overlap inputs other than h_out = h
  * with the same stride.
  */

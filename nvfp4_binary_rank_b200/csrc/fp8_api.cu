@@ -19,7 +19,7 @@ int status_of(cudaError_t e) { return e == cudaSuccess ? BILOCO_OK : BILOCO_ERR_
 
 bool bad_type(int t) { return t != BILOCO_TYPE_BF16 && t != BILOCO_TYPE_F32; }
 
-constexpr int kMaxDim = 1 << 24;
+constexpr int kMaxDim = 1 << 24, kMaxRows = 1 << 30;
 
 }  // namespace
 
@@ -28,7 +28,8 @@ extern "C" {
 int biloco_fp8_quant_act(const void* x_bf16, long long ldx, int M, int K, uint8_t* codes, float* scales,
                          biloco_stream_t stream) {
   if (M < 0 || (M > 0 && (!x_bf16 || !codes || !scales))) return BILOCO_ERR_ARG;
-  if (K < 16 || K % 16 || K > kMaxDim || ldx < K || ldx % 8) return BILOCO_ERR_SHAPE;
+  if (K < 16 || K % 16 || K > kMaxDim || ldx < K || ldx % 8 || M > kMaxRows) return BILOCO_ERR_SHAPE;
+  if (static_cast<long long>(M) * ((K + 511) / 512) > 0x7FFFFFFFLL) return BILOCO_ERR_SHAPE;
   if (off(x_bf16, 16) || off(codes, 16) || off(scales, 4)) return BILOCO_ERR_ALIGN;
   const int d = check_device();
   if (d || M == 0) return d;
@@ -70,7 +71,7 @@ int biloco_block_norm(const void* y_bf16, long long ldy, const void* h, long lon
   if ((!y_bf16 && !h) || (!y_bf16 && (post_weight || gate)) || (!h_out && !x_bf16 && !codes) ||
       ((x_bf16 || codes) && !pre_weight) || (pre_weight && !x_bf16 && !codes) || (!codes != !scales))
     return M == 0 ? BILOCO_OK : BILOCO_ERR_ARG;
-  if (D < 8 || D % 8 || D > BILOCO_NORM_MAX_D || (codes && D % 16)) return BILOCO_ERR_SHAPE;
+  if (D < 8 || D % 8 || D > BILOCO_NORM_MAX_D || (codes && D % 16) || M > kMaxRows) return BILOCO_ERR_SHAPE;
   if ((y_bf16 && (ldy < D || ldy % 8)) || (h && (ldh < D || ldh % 8)) || (h_out && (ldho < D || ldho % 8)))
     return BILOCO_ERR_SHAPE;
   if (gate && (gate_rows < 1 || M % gate_rows)) return BILOCO_ERR_SHAPE;

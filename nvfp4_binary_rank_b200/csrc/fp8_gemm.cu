@@ -35,7 +35,6 @@
 #include "../../include/biloco.h"
 #include "fp8_dev.cuh"
 #include "fp8_ops.h"
-#include "fp8_promote.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -366,7 +365,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       }
     } else if (warp == 1) {
       if (half == 0 && elect_one()) {
-        // ---- MMA issuer (the pair's first CTA)
+        // ---- MMA issuer (the pair's first CTA).  It needs the activation, and its waits are
+      // bounded: they begin when the kernel before this one has ended.
+      griddep_wait();
         const uint32_t idesc =
             (1u << 4) | (static_cast<uint32_t>(C::kN >> 3) << 17) | (static_cast<uint32_t>(kPair ? 16 : 8) << 24);
         const SmemDesc a0 = make_sdesc(smem, 16, 1024, 2), b0 = make_sdesc(smem + 16384, 16, 1024, 2);
@@ -682,6 +683,7 @@ cudaError_t launch_instance(const CUtensorMap& ta, const CUtensorMap& tb, Fp8Gem
     if (tiles <= d.clusters[q]) split = q;
   p.split = split;
   const long long slots = d.clusters[1];
+  if (slots < 1) return cudaErrorCooperativeLaunchTooLarge;
   const unsigned groups = static_cast<unsigned>(split > 1 ? tiles * split : tiles < slots ? tiles : slots);
   return launch_pdl(kernel, groups * C::kPair, C::kThreads, C::kSmem, split * C::kPair, s, ta, tb, p);
 }
@@ -729,6 +731,7 @@ int run_fp8_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const fl
   else if (bn == 32) e = launch_instance<true, 32>(tw, tx, p, s);
   else if (bn == 64) e = launch_instance<true, 64>(tw, tx, p, s);
   else e = launch_instance<true, 128>(tw, tx, p, s);
+  if (e == cudaErrorCooperativeLaunchTooLarge) return BILOCO_ERR_RESIDENCY;
   return e == cudaSuccess ? BILOCO_OK : BILOCO_ERR_CUDA;
 }
 

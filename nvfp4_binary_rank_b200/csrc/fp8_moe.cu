@@ -77,7 +77,7 @@ __device__ __forceinline__ uint32_t f16x2_from_e4m3x2(uint32_t codes) {
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
 // Exponent e with 2^e <= |largest| < 2^(e+1), from the FP32 bits of a maximum; kept where
-// 2^(14 - e) and 2^(e - 14) are normal numbers.
+// 2^-e, 2^(14 - e) and 2^(e - 14) are normal numbers.
 __device__ __forceinline__ int exponent_of(uint32_t bits) {
   return min(max(static_cast<int>(bits >> 23) - 127, -100), 127);
 }
@@ -104,11 +104,11 @@ struct RouterPiece {
 };
 
 // Order-preserving integer key of a score: larger is better, 0 stands for "taken".  A score
-// that is no number gets 1, below every number.
+// that is no number gets 1, below every number; -0 counts as 0.
 __device__ __forceinline__ unsigned long long order_key(double v) {
-  const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(v));
   if (isnan(v)) return 1;
-  return (b >> 63) ? ~b + 1 : b | 0x8000000000000001ull;
+  const unsigned long long b = static_cast<unsigned long long>(__double_as_longlong(v + 0.0));
+  return (b >> 63) ? ~b : b | 0x8000000000000000ull;
 }
 
 // A cluster of eight CTAs serves kTok tokens: each CTA scores an eighth of the experts for
