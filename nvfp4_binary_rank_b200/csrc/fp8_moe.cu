@@ -18,9 +18,10 @@
 //
 // Four kernels on one stream, each launched while the one before it ends:
 //   route    scores in FP32 with compensated sums, top-k, the token rows in FP16
-//   product  (up) per (expert, 16 hidden columns): gate and up rows over the whole of D, split
-//            over the CTA's warps; h in FP16 with an exponent per 8 columns, and the row's maximum
-//   product  (down) per (expert, 64 output rows): each (token, expert) pair's share of y in FP32
+//   product  (up) per 16 tokens of an expert and 16 hidden columns: the gate and up rows over the
+//            whole of D; h in FP16 with an exponent per 8 columns, and the row's maximum
+//   product  (down) per 16 tokens of an expert and 32 output rows: each (token, expert) pair's
+//            share of y in FP32
 //   combine  the shares of a token added in the order its experts were picked
 // Nothing is added by atomics but a maximum, so the result does not depend on timing.
 #include <algorithm>
@@ -296,62 +297,66 @@ moe_route_kernel(const __grid_constant__ MoeArgs a) {
 // ------------------------------------------------------------------ experts' token lists
 
 struct Lists {
-  int count[kMoeMaxExperts + kMoeMaxShared];       // tokens of an expert
-  int begin[kMoeMaxExperts + kMoeMaxShared];       // its first place in `pairs`
-  int active[kMoeMaxExperts + kMoeMaxShared];      // experts with tokens, ascending
-  int pairs[kMoeMaxPairs];                         // t * KT + j, grouped by expert
-  int nact;
+  unsigned long long mask[kMoeMaxExperts + kMoeMaxShared];   // tokens of an expert (it has each once)
+  uint16_t begin[kMoeMaxExperts + kMoeMaxShared];            // its first place in `pairs`
+  uint16_t pairs[kMoeMaxPairs];                              // t * KT + j, grouped by expert
+  uint16_t unit[kMoeMaxExperts + kMoeMaxShared + kMoeMaxPairs / 16];   // expert * 4 + its 16 tokens
+  int units;
 };
 
-// Every CTA groups the (token, expert) pairs by expert for itself.
+// Every CTA groups the (token, expert) pairs by expert for itself.  All find the same order, since
+// an expert's units are different CTAs' work.
 __device__ __forceinline__ void build_lists(Lists& l, const MoeArgs& a) {
   const int tid = threadIdx.x, n = a.E + a.shared, P = a.T * (a.k + a.shared);
   if (a.T == 1) {                                  // every pair is an expert of its own
     if (tid < P) {
       const int e = __ldcg(a.pair_id + tid);
-      l.active[tid] = e;
-      l.pairs[tid] = tid;
-      l.begin[e] = tid;
-      l.count[e] = 1;
+      l.unit[tid] = static_cast<uint16_t>(e * 4);
+      l.pairs[tid] = static_cast<uint16_t>(tid);
+      l.begin[e] = static_cast<uint16_t>(tid);
+      l.mask[e] = 1;
     }
-    if (tid == 0) l.nact = P;
+    if (tid == 0) l.units = P;
     __syncthreads();
     return;
   }
-  for (int e = tid; e < n; e += kThreads) l.count[e] = 0;
+  for (int e = tid; e < n; e += kThreads) l.mask[e] = 0;
   __syncthreads();
-  int pos[kMoeMaxPairs / kThreads], id[kMoeMaxPairs / kThreads];
+  const int KT = a.k + a.shared;
+  int id[kMoeMaxPairs / kThreads];
 #pragma unroll
   for (int i = 0; i < kMoeMaxPairs / kThreads; ++i) {
     const int q = i * kThreads + tid;
     if (q < P) {
       id[i] = __ldcg(a.pair_id + q);
-      pos[i] = atomicAdd(&l.count[id[i]], 1);
+      // in 32-bit halves, which shared memory does by itself; 64 bits at once are a loop of exchanges
+      atomicOr(reinterpret_cast<uint32_t*>(&l.mask[id[i]]) + q / KT / 32, 1u << (q / KT & 31));
     }
   }
   __syncthreads();
   if (tid < 32) {
-    int base = 0, na = 0;
+    int base = 0;                                  // sums of tokens and, 16 bits higher, of units
     for (int e0 = 0; e0 < n; e0 += 32) {
-      const int e = e0 + tid, c = e < n ? l.count[e] : 0;
-      int s = c;
+      const int e = e0 + tid, c = e < n ? __popcll(l.mask[e]) : 0, own = c | (c + 15) / 16 << 16;
+      int s = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xFFFFFFFFu, s, o);
         if (tid >= o) s += v;
       }
-      const uint32_t has = __ballot_sync(0xFFFFFFFFu, c > 0);
-      if (e < n) l.begin[e] = base + s - c;
-      if (c > 0) l.active[na + __popc(has & ((1u << tid) - 1))] = e;
+      const int before = base + s - own;
+      if (e < n) l.begin[e] = static_cast<uint16_t>(before);
+      for (int i = 0; i < (c + 15) / 16; ++i) l.unit[(before >> 16) + i] = static_cast<uint16_t>(e * 4 + i);
       base += __shfl_sync(0xFFFFFFFFu, s, 31);
-      na += __popc(has);
     }
-    if (tid == 0) l.nact = na;
+    if (tid == 0) l.units = base >> 16;
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kMoeMaxPairs / kThreads; ++i)
-    if (i * kThreads + tid < P) l.pairs[l.begin[id[i]] + pos[i]] = i * kThreads + tid;
+  for (int i = 0; i < kMoeMaxPairs / kThreads; ++i) {
+    const int q = i * kThreads + tid;
+    if (q < P) l.pairs[l.begin[id[i]] + __popcll(l.mask[id[i]] & ((1ull << (q / KT)) - 1))] = static_cast<uint16_t>(q);
+  }
   __syncthreads();
 }
 
@@ -367,10 +372,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 
 // A warp's stream of weights: runs of 64 along K of kTiles 8-row tiles, copied to shared
 // memory kStages - 1 runs ahead.  A lane reads back only what it copied itself, so the
-// stream needs no barriers, and unlike registers its depth costs nothing: 16 warps of an SM
-// keep 96 KB in flight.  (Held in registers one block ahead, the kernels spilled and the up
-// kernel ran at a seventh of the memory rate.)
-constexpr int kStages = 4;
+// stream needs no barriers.  (Held in registers one block ahead, the kernels spilled and the up
+// kernel ran at a seventh of the memory rate.)  What shared memory leaves of an SM's 256 KB is
+// the L1 that the warps share their activations through, and it counts for more than a deeper
+// stream: 64 tokens, 65 experts of 3 x 5120 x 2048, took 437 us with four stages and a second
+// buffer of sums (34 KB of L1), 420 without the buffer, 416 with three stages (107 KB); an L2
+// prefetch of 256 bytes rather than 128 is worth 441 -> 416.
+constexpr int kStages = 3;
 constexpr int kRunBytes = kTiles * 512;
 constexpr int kStreamBytes = kWarps * kStages * kRunBytes;
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst, const void* src, bool in) {
@@ -407,8 +415,7 @@ __device__ __forceinline__ void mma_run(float (&b0)[2][4], float (&b1)[2][4], ui
 __device__ __forceinline__ void load_run(uint32_t (&v)[8], const uint16_t* p, bool has) {
   asm volatile(
       "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %9, 0;\n\t"
-      "@q ld.global.v4.u32 {%0,%1,%2,%3}, [%8];\n\t"
-      "@q ld.global.v4.u32 {%4,%5,%6,%7}, [%8+16];\n\t}"
+      "@q ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\t}"
       : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])
       : "l"(p), "r"(static_cast<uint32_t>(has)));
 }
@@ -423,15 +430,23 @@ __device__ __forceinline__ void scale_hidden(uint32_t (&v)[8], int2 e, int row_e
 }
 
 // The products of both layers.  A row group is four tiles: for the up layer the gate and the
-// up rows of 16 hidden columns, for the down layer 32 output rows.  An item is an expert and
-// kGroups row groups; kSplit warps share a group's blocks along K and meet in shared memory,
-// the CTAs walk through the items side by side, so that all of them read the same few
-// megabytes at a time: with a run of items of its own for each CTA, 1.4 GB of experts took
-// twice as long (the pages of 296 places do not fit the address caches).  More than 16 tokens
-// of an expert take further passes over the item's weights, which then come from L2.
+// up rows of 16 hidden columns, for the down layer 32 output rows.  A unit is up to 16 tokens of
+// an expert, an item a unit and kGroups row groups; kSplit warps share a group's blocks along K
+// and meet in shared memory.  The CTAs walk through the items side by side, so that all of them
+// read the same few megabytes at a time: with a run of items of its own for each CTA, 1.4 GB of
+// experts took twice as long (the pages of 296 places do not fit the address caches).  More
+// than 16 tokens of an expert are several units, whose weights all but the first read from L2; as
+// further passes of one CTA they left the others waiting at the end (64 tokens with a shared
+// expert: 470 -> 437 us).
 //
 // kOne (down, one token): a cluster of the token's experts owns 64 output rows; the shares meet
 // in distributed shared memory and there is no combine kernel.
+//
+// Measured, device time past L2: 64 tokens, 65 experts of 3 x 5120 x 2048 (2.05 GB): 416 us for
+// the layer, 4.9 TB/s of weights; 16 tokens, 32 + 1 experts of 3 x 4096 x 2048: 135 us, 5.4 TB/s; one
+// token, 8 experts of 3 x 2048 x 1024: 26 us, of which the router takes 7 and each product waits for
+// the kernel before it.  Bound by the latency of the loads: 16 warps an SM, each with 4 KB of
+// weights on the way, leave the schedulers idle for 60% of the time.
 template <bool kUp, int kSplit, bool kOne = false>
 __global__ void __launch_bounds__(kThreads, 2)
 moe_product_kernel(const __grid_constant__ MoeArgs a) {
@@ -439,7 +454,7 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
   __shared__ float own[kOne ? 32 * kGroups : 1];
   extern __shared__ __align__(16) uint8_t stream[];
   __shared__ Lists l;
-  __shared__ float4 red[2][kWarps][kTiles][32];
+  __shared__ float4 red[2][kWarps][kTiles / 2][32];
   if (kUp) griddep_wait();
   // in the up kernel after the wait: the down kernel may then read the route's results at once
   griddep_launch_dependents();
@@ -448,7 +463,7 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
   const int K = kUp ? a.D : a.F, F = a.F, D = a.D, KT = a.k + a.shared;
   const int KB = (K + 127) / 128, NB = ((kUp ? 2 * F : D) + 127) / 128;
   const int groups = kUp ? F / 16 : (D + 31) / 32, per = (groups + kGroups - 1) / kGroups;   // items of an expert
-  const int items = l.nact * per, stride = kOne ? items : static_cast<int>(gridDim.x);
+  const int items = l.units * per, stride = kOne ? items : static_cast<int>(gridDim.x);
   const int first = kOne ? static_cast<int>(cta_rank()) * per + static_cast<int>(blockIdx.x) / (a.k + a.shared)
                          : static_cast<int>(blockIdx.x);
   const int sub = warp / kSplit, kp = warp % kSplit;
@@ -458,12 +473,11 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
 
   // ---- the weight stream
   const uint32_t ring = smem_u32(stream) + warp * (kStages * kRunBytes) + lane * 16;
-  int ci = first, cp = 0, cr = 0, cslot = 0, ccount = 0;
+  int ci = first, cr = 0, cslot = 0;
   const uint8_t* cbase = nullptr;
   int o1 = 8 * K, o2 = kUp ? F * K : 16 * K, o3 = o2 + 8 * K;      // offsets of tiles 1 to 3
   auto seek = [&] {
-    const int act = ci / per, e = l.active[act], grp = min((ci - act * per) * kGroups + sub, groups - 1);
-    ccount = l.count[e];
+    const int u = ci / per, e = l.unit[u] >> 2, grp = min((ci - u * per) * kGroups + sub, groups - 1);
     const int n = grp * (kUp ? 16 : 32);
     cbase = W + (static_cast<long long>(e) * (kUp ? 2 * F : D) + n + g) * K + b0 * 128 + t4 * 16;
     if (!kUp && n + 32 > D) {                       // the matrix ends inside the group: a tile twice
@@ -484,11 +498,7 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
       cp_async16_or_zero(dst + 1536, src + o3, in);
       if (++cr == runs) {
         cr = 0;
-        cp += 16;
-        if (cp >= ccount) {
-          cp = 0;
-          if ((ci += stride) < items) seek();
-        }
+        if ((ci += stride) < items) seek();
       }
     }
     cp_async_commit();
@@ -502,7 +512,7 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
 
   int slot = 0;
   // One pass over an item for `cnt` tokens, at most 8 or (kWide) 16.
-  auto pass = [&](auto wide_t, int e, int grp0, const int* pairs, int cnt, float4 (*sums)[kTiles][32], int step) {
+  auto pass = [&](auto wide_t, int e, int grp0, const uint16_t* pairs, int cnt, int step, bool sync) {
     constexpr bool kWide = decltype(wide_t)::value;
     constexpr int kHalves = kWide ? 2 : 1;
     // this lane's token of either eight, as the products' second operand
@@ -586,11 +596,12 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
           if (kWide) out[1][i][j] = fmaf(k1[i][j], i ? s1 : s0, out[1][i][j]);
         }
     }
+    if (sync) __syncthreads();
 #pragma unroll
     for (int h = 0; h < kHalves; ++h)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
-        sums[warp][h * 2 + i][lane] = make_float4(out[h][i][0], out[h][i][1], out[h][i][2], out[h][i][3]);
+        red[(step + h) & 1][warp][i][lane] = make_float4(out[h][i][0], out[h][i][1], out[h][i][2], out[h][i][3]);
     __syncthreads();
     if (kUp) {
       // a warp (in turn) for each group and eight tokens: product 0 are the gate rows, product 1 the up rows
@@ -599,7 +610,7 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
         float gs[4] = {0, 0, 0, 0}, us[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < kSplit; ++w) {
-          const float4 p = sums[grp * kSplit + w][2 * h][lane], q = sums[grp * kSplit + w][2 * h + 1][lane];
+          const float4 p = red[(step + h) & 1][grp * kSplit + w][0][lane], q = red[(step + h) & 1][grp * kSplit + w][1][lane];
           gs[0] += p.x; gs[1] += p.y; gs[2] += p.z; gs[3] += p.w;
           us[0] += q.x; us[1] += q.y; us[2] += q.z; us[3] += q.w;
         }
@@ -634,7 +645,7 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
         float v[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < kSplit; ++w) {
-          const float4 p = sums[grp * kSplit + w][h * 2 + i][lane];
+          const float4 p = red[(step + h) & 1][grp * kSplit + w][i][lane];
           v[0] += p.x; v[1] += p.y; v[2] += p.z; v[3] += p.w;
         }
 #pragma unroll
@@ -656,16 +667,17 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
       }
     }
   };
-  for (int it = first, p0 = 0, step = 0; it < items; ++step) {
-    const int act = it / per, e = l.active[act], grp0 = (it - act * per) * kGroups;
-    const int cnt = min(16, l.count[e] - p0);
-    const int* pairs = l.pairs + l.begin[e] + p0;
-    const bool more = p0 + 16 < l.count[e];
-    // Two buffers: the barrier of the step between orders a buffer's next use after its reads.
-    if (cnt > 8) pass(std::true_type(), e, grp0, pairs, cnt, red[step & 1], step);
-    else pass(std::false_type(), e, grp0, pairs, cnt, red[step & 1], step);
-    p0 = more ? p0 + 16 : 0;
-    if (!more) it += stride;
+  bool wide = false;
+  for (int it = first, step = 0; it < items; it += stride, ++step) {
+    const int at = it / per, u = l.unit[at], e = u >> 2, p0 = (u & 3) * 16, grp0 = (it - at * per) * kGroups;
+    const int cnt = min(16, __popcll(l.mask[e]) - p0);
+    const uint16_t* pairs = l.pairs + l.begin[e] + p0;
+    // Two buffers of eight tokens' sums: the barrier of the step between orders a buffer's next
+    // use after its reads, unless one of the two steps uses both.
+    const bool sync = cnt > 8 || wide;
+    wide = cnt > 8;
+    if (wide) pass(std::true_type(), e, grp0, pairs, cnt, step, sync);
+    else pass(std::false_type(), e, grp0, pairs, cnt, step, sync);
   }
   if (kOne) {
     cluster_barrier();
@@ -718,11 +730,12 @@ struct MoeSetup {
 // How many warps share a row group's K.  With few, an item is larger and its barrier and
 // joining cost less per byte; with many, the items deal out more evenly over the CTAs.  The
 // estimate, in units of a warp's time for one block of 128: a warp's blocks plus 1.5 for the
-// end of an item, times the rounds of items plus 1.5.  Measured, us of a layer of 64 tokens and
-// 65 experts with 8, 4, 2 warps in the up kernel: 474, 461, 497 (3 x 5120 x 2048), 181, 197,
-// 225 (3 x 5120 x 512); in the down kernel 497, 474, 476 and 218, 181, 178.
+// end of an item, times the rounds of items plus one.  Measured, us of a whole layer with 8, 4, 2
+// warps in the up kernel: 435, 416, 437 (64 tokens, 65 experts of 3 x 5120 x 2048), 94, 81, 81
+// (16 tokens, 64 of 3 x 2048 x 1024), 26.5, 28.5, 28 (one token, 8 of 3 x 2048 x 1024); with 4, 2
+// in the down kernel 430, 416 and 85, 81.
 template <bool kUp>
-cudaError_t launch_product(const MoeArgs& a, int experts, cudaStream_t s) {
+cudaError_t launch_product(const MoeArgs& a, int units, cudaStream_t s) {
   const long long slots = 2LL * num_sms();
   const int KB = ((kUp ? a.D : a.F) + 127) / 128, groups = kUp ? a.F / 16 : (a.D + 31) / 32;
   int best = 8;
@@ -730,8 +743,8 @@ cudaError_t launch_product(const MoeArgs& a, int experts, cudaStream_t s) {
   long long best_items = 0;
   for (int split = 8; split >= 2; split /= 2) {
     const int per = (groups + kWarps / split - 1) / (kWarps / split);
-    const long long items = static_cast<long long>(experts) * per;
-    const double c = ((items + slots - 1) / slots + 1.5) * ((KB + split - 1) / split + 1.5);
+    const long long items = static_cast<long long>(units) * per;
+    const double c = ((items + slots - 1) / slots + 1.0) * ((KB + split - 1) / split + 1.5);
     if (split == 8 || c < cost) {
       best = split;
       cost = c;
@@ -801,15 +814,15 @@ cudaError_t launch_fp8_moe(MoeArgs& a, cudaStream_t s) {
                      : launch_pdl(moe_route_kernel<4, false>, grid, kThreads, sm, kRouteCtas, s, a);
   if (e != cudaSuccess) return e;
 
-  const int experts = std::min(a.T * a.k, a.E) + a.shared;
-  e = launch_product<true>(a, experts, s);
+  const int units = std::min(a.T * a.k, a.E) + a.shared * ((a.T + 15) / 16);     // about
+  e = launch_product<true>(a, units, s);
   if (e != cudaSuccess) return e;
   if (a.T == 1 && a.k + a.shared <= 8) {
     const unsigned n = static_cast<unsigned>(a.k + a.shared);
     return launch_pdl(moe_product_kernel<false, 4, true>, static_cast<unsigned>((a.D + 63) / 64) * n, kThreads, kStreamBytes, n,
                       s, a);
   }
-  e = launch_product<false>(a, experts, s);
+  e = launch_product<false>(a, units, s);
   if (e != cudaSuccess) return e;
   return launch_pdl(moe_combine_kernel, static_cast<unsigned>((a.T * (a.D / 4) + kThreads - 1) / kThreads), kThreads, 0, 1,
                     s, a);
