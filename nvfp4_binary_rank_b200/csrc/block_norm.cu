@@ -11,7 +11,9 @@
 // 696 instructions a warp and row and was bound by them).  CTAs stay: each walks over rows,
 // and the loads of its next row are under way from the middle of the current one, when the
 // registers of that are free.  y and h pass by L1, which so keeps the weights.
-// Measured at 8192 x 5120 with FP8 output (295 MB): one CTA per row 85 us, this 65 us.
+// Measured at 8192 x 5120 with FP8 output (295 MB): one CTA per row 85 us, this 65 us (4.5 TB/s,
+// instructions issued in 70% of the clocks); one row of 5120 takes 3.0 us, two reductions over a
+// CTA and the loads before them.
 // Both sums of squares are FP32; x is computed from the unrounded h', so h' and x are each
 // rounded once.
 #include <algorithm>
@@ -267,9 +269,14 @@ cudaError_t launch_one(const BlockNormArgs& a, cudaStream_t s) {
 
 template <bool kHf32, bool kWf32>
 cudaError_t launch_typed(const BlockNormArgs& a, cudaStream_t s) {
-  // A few rows: one piece a thread, the shortest way through a row.  Many: two, so that
-  // several rows are under way on an SM.
-  if (a.D <= 2048 || (a.D <= 8192 && a.M <= num_sms())) return launch_one<1, 1024, kHf32, kWf32>(a, s);
+  // Short rows, and as many as one round of CTAs takes: one piece a thread, the shortest way
+  // through a row.  More: two, so that several rows are under way on an SM.  Four where two
+  // need more than 512 threads.  Measured with FP8 output, us with one and two pieces: 2.6 and 3.1
+  // (1 x 5120), 3.4 and 4.0 (148 x 5120), 4.6 and 4.3 (149 x 5120), 92 and 65 (8192 x 5120); 3.6 and
+  // 4.1 (592 x 2048), 27.4 and 24.5 (8192 x 2048); 14.5 and 14.4 (8192 x 1024), 8.0 and 9.0
+  // (8192 x 512).  Four pieces: 94 (8192 x 5120).
+  const int threads = (a.D / 8 + 31) / 32 * 32;
+  if (a.D <= 1024 || (threads <= 1024 && a.M <= 1024 / threads * num_sms())) return launch_one<1, 1024, kHf32, kWf32>(a, s);
   if (a.D <= 8192) return launch_one<2, 512, kHf32, kWf32>(a, s);
   return launch_one<4, 1024, kHf32, kWf32>(a, s);
 }

@@ -17,6 +17,17 @@
 //   swapped form (up to 128 tokens): the MMA's 128 rows are weight rows and its columns
 //     tokens, so a decode batch is not padded to 128 rows; scales vary over the columns.
 //     Bound by reading the weight.
+// Measured, device time past L2 (M tokens, N x K weight):
+//   4096, 13824 x 5120: 268 us, 2.16 PFLOP/s.  A block of 128 takes about 790 clocks, of which its
+//     MMAs are 513; the rest is the chain commit - read back - release of an accumulator.  Runs
+//     of seconds are held by the power limit at about 310 us.
+//   512, 5120 x 5120: 23.5 us;  333, 1000 x 2064: 10.4 us (latency of one chain of blocks)
+//   1, 5120 x 5120: 8.6 us, 3.1 TB/s;  16, 13824 x 5120: 15.3 us, 4.7 TB/s: each CTA's part of
+//     the weight is a few blocks, so starting up and joining the parts weigh as much as the stream.
+// What was slower: rows form with one accumulator pair of 256 columns (275 us at 4096 tokens, 29.0
+// at 512), without a pair of CTAs (128 x 256 tiles: 308), without moving registers (278), with
+// eight promoting warps (279); swapped form with three smaller CTAs an SM (1 token 9.1 us, 16
+// tokens 17.1).
 // The token scales come through a ring in shared memory that a warp of its own fills a few
 // blocks ahead: loaded by the promoting warps themselves, one block ahead, their latency
 // (about 1000 clocks under load) set the pace of the rows form.
@@ -111,8 +122,8 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
 }
 
 // One lane of a converged warp.  The compiler knows that a branch on it leaves a single
-// thread, so the operands of tcgen05 and TMA instructions go to uniform registers
-// directly; after a branch on `lane == 0` each of them cost about 130 clocks.
+// thread, so the operands of tcgen05 and TMA instructions go to uniform registers directly:
+// four MMAs and two commits took about 300 clocks, after a branch on `lane == 0` 500.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
@@ -164,8 +175,8 @@ struct Cfg {
   static constexpr int kRegTotal = 128 * kGroups * kRegPromote + 128 * kRegOther;
   static constexpr int kPitch = kSwap ? 128 : kBN + 4;         // floats per row of the split-K exchange
   static_assert(kStages * kStageBytes >= (kSwap ? kBN : 128) * kPitch * 4, "the exchange reuses the stages");
+  static_assert(kSwap || kRegTotal <= kThreads * kRegLaunch, "more registers than the launch has");
   // a stage's "done" phase must be seen by the promoting warps before the next one ends
-  static_assert(kSwap || kRegTotal <= kThreads * kRegLaunch, "");
   static_assert(kBufs <= kStages && kTmemCols * kCtasPerSm <= 512, "");
 };
 
@@ -366,8 +377,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
     } else if (warp == 1) {
       if (half == 0 && elect_one()) {
         // ---- MMA issuer (the pair's first CTA).  It needs the activation, and its waits are
-      // bounded: they begin when the kernel before this one has ended.
-      griddep_wait();
+        // bounded: they begin when the kernel before this one has ended.
+        griddep_wait();
         const uint32_t idesc =
             (1u << 4) | (static_cast<uint32_t>(C::kN >> 3) << 17) | (static_cast<uint32_t>(kPair ? 16 : 8) << 24);
         const SmemDesc a0 = make_sdesc(smem, 16, 1024, 2), b0 = make_sdesc(smem + 16384, 16, 1024, 2);
@@ -718,6 +729,11 @@ int run_fp8_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const fl
   p.y_f32 = y_f32;
   const unsigned long long bits = reinterpret_cast<uintptr_t>(y) | static_cast<unsigned long long>(N) * (y_f32 ? 4 : 2);
   p.vec = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : 2;
+  // Swapped up to one MMA's 128 columns.  Across the border, us at 5120 x 5120, 13824 x 5120 and
+  // 1024 x 5120: 13.0, 22.7, 8.5 at 128 tokens (swapped), 15.7, 23.5, 12.3 at 129 (rows form, half
+  // of its 256 rows idle).  Columns are the next power of two from 16 on: 8.9, 15.3, 5.1 at 16
+  // tokens and 9.4, 17.1, 5.3 at 17; 9.8, 17.7, 5.6 at 32 and 11.1, 21.9, 6.4 at 33; 11.8, 22.1, 7.0 at
+  // 64 and 12.1, 22.1, 7.6 at 65.
   const bool swap = M <= 128;
   const int bn = !swap ? 256 : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   p.tiles_a = swap ? p.NB : (M + 255) / 256;
