@@ -364,8 +364,9 @@ int biloco_block_norm(const void *y_bf16, long long ldy, const void *h, long lon
  * is picked last.  The products are FP16 x E4M3 with FP32 sums: rows of x are scaled into
  * FP16 exactly (BF16 values more than 2^29 below the row's largest lose bits), the hidden
  * values are rounded to FP16.  A token with an infinity or NaN spoils only its own row.
- * Four kernels with programmatic dependent launch; w2 may be read before the kernel before
- * them on the stream has ended (see biloco_gemm on what must not write the weight).
+ * Four kernels (three for one token) with programmatic dependent launch; router and w2 may be
+ * read before the kernel before them on the stream has ended (see biloco_gemm on what must
+ * not write the weight).
  * The result depends only on the operands and the shape.
  */
 #define BILOCO_MOE_MAX_T 64

@@ -127,7 +127,9 @@ def fp8_pack_weight(W: torch.Tensor, stream=None):
 def fp8_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
              out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """y[m, n] = sum_b x_scales[b, m] w_scales[n/128, b] (x[m] . w[n])_b over blocks b of 128
-    along K, for any number of rows; y is bfloat16 or float32."""
+    along K, for any number of rows; y is bfloat16 or float32.  w_codes may be read while the kernel
+    before this one on the stream still runs: no call of this library but fp8_pack_weight may have
+    written it just before."""
     if stream is None and (out is not None or out_dtype in _TYPE):
         r = (_fast or _load_fast()).gemm(x_codes, x_scales, w_codes, w_scales, out,
                                          (out_dtype if out is None else getattr(out, "dtype", None)) is _F32)
@@ -272,7 +274,9 @@ def fp8_moe(x: torch.Tensor, router: torch.Tensor, w13: torch.Tensor, w13_scales
     and w2 [n, D, F] with their scales from fp8_pack_weight.  The n - E last experts are
     shared: they serve every token with weight 1.  `score` is "softmax" (over the experts)
     or "sigmoid"; bias float32 [E] is added for the choice only.  Returns (y bfloat16
-    [T, D], ids int32 [T, top_k], weights float32 [T, top_k])."""
+    [T, D], ids int32 [T, top_k], weights float32 [T, top_k]).  router and w2 may be read while the
+    kernel before this call on the stream still runs: no call of this library but fp8_pack_weight
+    may have written them just before."""
     if stream is None and score in _SCORE:
         r = (_fast or _load_fast()).moe(x, router, w13, w13_scales, w2, w2_scales, bias, top_k, _SCORE[score], bool(renorm),
                                         route_scale)

@@ -14,14 +14,14 @@
 //     columns').  A pair of CTAs (cta_group::2) computes 256 tokens x 256 weight rows, each
 //     CTA loading 128 rows of either operand: 32 KB per block and SM instead of 48.
 //     Persistent over tiles.
-//   swapped form (up to 128 tokens): the MMA's 128 rows are weight rows and its columns
-//     tokens, so a decode batch is not padded to 128 rows; scales vary over the columns.
-//     Bound by reading the weight.
+//   swapped form (up to 128 tokens, and small products): the MMA's 128 rows are weight rows and
+//     its columns tokens, so a decode batch is not padded to 128 rows; scales vary over the
+//     columns.  Bound by reading the weight.
 // Measured, device time past L2 (M tokens, N x K weight):
 //   4096, 13824 x 5120: 268 us, 2.16 PFLOP/s.  A block of 128 takes about 790 clocks, of which its
 //     MMAs are 513; the rest is the chain commit - read back - release of an accumulator.  Runs
 //     of seconds are held by the power limit at about 310 us.
-//   512, 5120 x 5120: 23.5 us;  333, 1000 x 2064: 10.4 us (latency of one chain of blocks)
+//   512, 5120 x 5120: 23.5 us;  333, 1000 x 2064: 9.2 us (latency of one chain of blocks)
 //   1, 5120 x 5120: 8.6 us, 3.1 TB/s;  16, 13824 x 5120: 15.3 us, 4.7 TB/s: each CTA's part of
 //     the weight is a few blocks, so starting up and joining the parts weigh as much as the stream.
 // What was slower: rows form with one accumulator pair of 256 columns (275 us at 4096 tokens, 29.0
@@ -36,7 +36,8 @@
 // leaves its FP32 sums in its own shared memory and the cluster adds them in rank order
 // over distributed shared memory, so the result does not depend on timing and no
 // workspace or counter outlives the call.
-#include <atomic>
+#include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 
@@ -436,7 +437,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       for (int t = first; ok && t < tiles; t += step) {
         int ta, tb;
         tile_at(t, p.tiles_a, p.tiles_b, ta, tb);
-        const int tok0 = kSwap ? 0 : ta * 256 + half * 128;
+        const int tok0 = kSwap ? tb * kBN : ta * 256 + half * 128;
         const int wblk = kSwap ? ta : tb * 2 + (lane & 1);
         const float* pw = p.ws + static_cast<long long>(min(wblk, p.NB - 1)) * p.KB;
         for (int kb = k0; ok && kb < k1; kb += 4) {
@@ -579,11 +580,11 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
         }
       } else if (ok) {
         if (kSwap) {
-          const int n = ta * 128 + row;
+          const int n = ta * 128 + row, m = tb * kBN + grp * C::kCols;
           if (n < p.N) {
 #pragma unroll
             for (int j = 0; j < C::kCols; ++j)
-              if (grp * C::kCols + j < p.M) store_one(p, static_cast<long long>(grp * C::kCols + j) * p.N + n, v[j]);
+              if (m + j < p.M) store_one(p, static_cast<long long>(m + j) * p.N + n, v[j]);
           }
         } else {
           const int tok = ta * 256 + half * 128 + row, n = tb * kBN + grp * C::kCols;
@@ -715,6 +716,33 @@ int fp8_take_status(cudaStream_t s) {
   return status;
 }
 
+// Columns of the swapped form's tiles.  Up to 32 tokens one tile takes all.  Above, small tiles
+// give a small problem more CTAs, and parts of K; large ones read the weight fewer times.  The
+// estimate, in units of one block's time in a tile of 128: the blocks of a CTA (as many as its SM
+// holds share it) and 7 for the rest, of which a tile of up to 32 columns takes 0.6, and the
+// operands of all tiles at 25 MB.  Measured, us with 32, 64, 128 columns: 5.3, 6.1, 7.9 (128 tokens,
+// 512 x 2064), 7.6, 8.8, 9.3 (64, 2048 x 5120), 10.2, 10.0, 10.3 (128, 2048 x 5120), 15.5, 11.8, 12.6 (64,
+// 5120 x 5120), 25.7, 21.1, 13.5 (128, 5120 x 5120), 15.9, 13.5, 10.7 (333, 1024 x 5120).
+static int swapped_columns(int M, int NB, int KB) {
+  if (M <= 32) return M <= 16 ? 16 : 32;
+  const int sms = num_sms();
+  int best = 0;
+  double cost = 0.0;
+  for (int bn = 32; bn <= 128; bn *= 2) {
+    const double tiles = static_cast<double>(NB) * ((M + bn - 1) / bn), slots = bn <= 64 ? 2.0 * sms : sms;
+    int split = 1;
+    while (split < 8 && split < KB && tiles * (split + 1) <= slots) ++split;
+    const double blocks = std::ceil(tiles / slots) * ((KB + split - 1) / split);
+    const double shared = std::max(1.0, std::min(tiles * split, slots) / sms);
+    const double c = (blocks * shared + 7.0) * (bn == 32 ? 0.6 : 1.0) + tiles * KB * (16384 + bn * 128) / 25e6;
+    if (!best || c < cost) {
+      best = bn;
+      cost = c;
+    }
+  }
+  return best;
+}
+
 int run_fp8_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const float* ws, void* y, bool y_f32, int M,
                  int N, int K, cudaStream_t s) {
   Fp8GemmParams p = {};
@@ -729,15 +757,15 @@ int run_fp8_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const fl
   p.y_f32 = y_f32;
   const unsigned long long bits = reinterpret_cast<uintptr_t>(y) | static_cast<unsigned long long>(N) * (y_f32 ? 4 : 2);
   p.vec = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : 2;
-  // Swapped up to one MMA's 128 columns.  Across the border, us at 5120 x 5120, 13824 x 5120 and
-  // 1024 x 5120: 13.0, 22.7, 8.5 at 128 tokens (swapped), 15.7, 23.5, 12.3 at 129 (rows form, half
-  // of its 256 rows idle).  Columns are the next power of two from 16 on: 8.9, 15.3, 5.1 at 16
-  // tokens and 9.4, 17.1, 5.3 at 17; 9.8, 17.7, 5.6 at 32 and 11.1, 21.9, 6.4 at 33; 11.8, 22.1, 7.0 at
-  // 64 and 12.1, 22.1, 7.6 at 65.
-  const bool swap = M <= 128;
-  const int bn = !swap ? 256 : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  // Rows form above 128 tokens, except where a quarter of the SMs hold the swapped form's tiles,
+  // so that four parts of K fit.  Across the borders, us at 5120 x 5120 and 1024 x 5120: 13.0 and 8.5
+  // at 128 tokens (swapped), 15.7 at 129 (rows form, half of its 256 rows idle; swapped 23.0), 12.3
+  // in the rows form and 9.6 swapped at 129; 2048 x 5120: 13.3 (rows) and 11.8 at 256 tokens, 32
+  // tiles, 14.4 and 15.0 at 333, 48 tiles.
+  const bool swap = M <= 128 || 4LL * p.NB * ((M + 127) / 128) <= num_sms();
+  const int bn = swap ? swapped_columns(M, p.NB, p.KB) : 256;
   p.tiles_a = swap ? p.NB : (M + 255) / 256;
-  p.tiles_b = swap ? 1 : (N + bn - 1) / bn;
+  p.tiles_b = swap ? (M + bn - 1) / bn : (N + bn - 1) / bn;
   if (static_cast<long long>(p.tiles_a) * p.tiles_b > 0x7FFFFFFFLL) return BILOCO_ERR_SHAPE;
   CUtensorMap tx, tw;
   if (!make_tmap(&tx, xq, K, M, swap ? bn : 128) || !make_tmap(&tw, wq, K, N, swap ? 128 : 64)) return BILOCO_ERR_CUDA;

@@ -226,6 +226,58 @@ def test_gemm_binding_refusals(nb):
         nb.fp8_quant_act(torch.zeros((32, 2), dtype=torch.bfloat16, device="cuda").t())
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,N,K", [
+    (129, 2500, 144), (257, 1700, 528), (333, 1800, 2064), (512, 1288, 272), (700, 1100, 400), (128, 2368, 144),
+    (129, 128, 2064), (300, 600, 272), (64, 200, 1040), (96, 130, 4096), (1000, 64, 256), (2048, 130, 384), (48, 5120, 256)])
+def test_gemm_parity_between_the_forms(nb, M, N, K, dtype):
+    """Few and many tiles above 128 tokens, and tiles of fewer columns than there are tokens."""
+    xc, xs, wc, ws = operands(nb, np.random.default_rng(M + 7 * N + K), M, N, K)
+    check(nb, xc, xs, wc, ws, nb.fp8_gemm(xc, xs, wc, ws, out_dtype=dtype))
+
+
+@pytest.mark.parametrize("M,N", [(300, 2000), (130, 500), (70, 130)])
+def test_gemm_one_hot_rows_are_exact_in_wide_products(nb, M, N):
+    K = 656
+    rng = np.random.default_rng(M + N)
+    codes = rng.integers(0, 0x7F, (N, K)).astype(np.uint8) | (rng.integers(0, 2, (N, K)).astype(np.uint8) << 7)
+    ws = 2.0 ** rng.integers(-8, 8, (-(-N // 128), 6)).astype(np.float32)
+    at = rng.integers(0, K, M)
+    xc = np.zeros((M, K), np.uint8)
+    xc[np.arange(M), at] = 0x38                                     # 1.0
+    xs = (2.0 ** rng.integers(-8, 8, (6, M))).astype(np.float32)
+    xg, wg = (torch.from_numpy(c).cuda().view(torch.float8_e4m3fn) for c in (xc, codes))
+    y = nb.fp8_gemm(xg, torch.from_numpy(xs).cuda(), wg, torch.from_numpy(ws).cuda(), out_dtype=torch.float32).cpu().numpy()
+    assert np.array_equal(y, (fp8.dequant_tiles(codes, ws)[:, at] * xs[at // 128, np.arange(M)]).T.astype(np.float32))
+
+
+def test_gemm_nan_and_inf_stay_in_their_rows_among_many_tiles(nb):
+    M, N, K = 300, 1800, 272
+    xc, xs, wc, ws = operands(nb, np.random.default_rng(3), M, N, K)
+    clean = nb.fp8_gemm(xc, xs, wc, ws)
+    xc.view(torch.uint8)[1, 130] = 0x7F
+    xs[0, 200] = float("inf")
+    wc.view(torch.uint8)[1150, 7] = 0xFF
+    y = nb.fp8_gemm(xc, xs, wc, ws)
+    assert bool(y[1].isnan().all()) and bool(y[:, 1150].isnan().all()) and not bool(y[200].isfinite().any())
+    keep = [m for m in range(M) if m not in (1, 200)]
+    cols = [n for n in range(N) if n != 1150]
+    assert torch.equal(y[keep][:, cols], clean[keep][:, cols])
+
+
+def test_gemm_many_calls_of_both_forms_in_a_row(nb):
+    sets = [operands(nb, np.random.default_rng(m), m, n, k)
+            for m, n, k in ((333, 1800, 2064), (700, 1100, 400), (333, 1000, 2064), (70, 512, 1040))]
+    want = [nb.fp8_gemm(*s) for s in sets]
+    for i in range(3000):
+        j = i % 4 if i % 100 < 50 else 0
+        y = nb.fp8_gemm(*sets[j])
+        if i % 100 == 49:
+            assert torch.equal(y, want[j])
+    assert torch.equal(y, want[j])
+    assert nb.last_error() == 0
+
+
 @pytest.mark.parametrize("M", [1, 50, 400])
 def test_streams_and_graphs(nb, M):
     """Two calls at once on two streams, and a captured quantise + product replayed on new inputs."""
