@@ -442,11 +442,14 @@ __device__ __forceinline__ void scale_hidden(uint32_t (&v)[8], int2 e, int row_e
 // kOne (down, one token): a cluster of the token's experts owns 64 output rows; the shares meet
 // in distributed shared memory and there is no combine kernel.
 //
-// Measured, device time past L2: 64 tokens, 65 experts of 3 x 5120 x 2048 (2.05 GB): 416 us for
-// the layer, 4.9 TB/s of weights; 16 tokens, 32 + 1 experts of 3 x 4096 x 2048: 135 us, 5.4 TB/s; one
-// token, 8 experts of 3 x 2048 x 1024: 26 us, of which the router takes 7 and each product waits for
-// the kernel before it.  Bound by the latency of the loads: 16 warps an SM, each with 4 KB of
-// weights on the way, leave the schedulers idle for 60% of the time.
+// Measured, device time past L2: 64 tokens, 65 experts of 3 x 5120 x 2048 (2.05 GB): 414 us for
+// the layer, 4.9 TB/s of weights; 16 tokens, 32 + 1 experts of 3 x 4096 x 2048: 135 us, 5.4 TB/s.  Bound
+// by the latency of the loads: 16 warps an SM, each with 4 KB of weights on the way, leave the
+// schedulers idle for 60% of the time.  One token, 8 experts of 3 x 2048 x 1024: 26 us, of which 14 are
+// there without the weights, in the chain of three kernels: 5 us in the router (2.4 of them for
+// the choice), 3 and 2 us in the first pass of the products, about twice the time of a second
+// one, since its instructions come from L2.  Passes without tokens while the kernel before runs, to
+// have the instructions, won 1 us there and cost 20 at 64 tokens.
 template <bool kUp, int kSplit, bool kOne = false>
 __global__ void __launch_bounds__(kThreads, 2)
 moe_product_kernel(const __grid_constant__ MoeArgs a) {
@@ -533,11 +536,14 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
     for (int h = 0; h < kHalves; ++h)
 #pragma unroll
       for (int i = 0; i < 2; ++i) out[h][i][0] = out[h][i][1] = out[h][i][2] = out[h][i][3] = 0.0f;
-    // activations, a run ahead of the products
-    uint32_t x[2][2][8];
-    int2 xe[2][2];
+    // Activations, kDepth - 1 runs ahead of the products, and scales two blocks ahead: where the
+    // weights have arrived a run takes less than a load from L2 (one token, 8 experts of 3 x 2048 x
+    // 1024: 27.2 -> 25.7 us against one run and one block).
+    constexpr int kDepth = kWide ? 2 : 4;
+    uint32_t x[kDepth][2][8];
+    int2 xe[kDepth][2];
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < kDepth; ++c)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         xe[c][h] = make_int2(0, 0);
@@ -557,44 +563,51 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
         if (!kUp && in) ve[h] = __ldcg(reinterpret_cast<const int2*>(a.hexp + (static_cast<long long>(row[h]) * F + k) / 8));
       }
     };
-    float s_gate = 0.0f, s_up = 0.0f;
-    if (runs) {
-      fetch(x[0], xe[0], 0);
-      s_gate = __ldg(S + b0);
-      s_up = __ldg(S + b0 + up_rows);
-    }
+    float s_gate[2] = {0.0f, 0.0f}, s_up[2] = {0.0f, 0.0f};
+    auto fetch_scales = [&](int i, int b) {
+      s_gate[i] = __ldg(S + b);
+      s_up[i] = __ldg(S + b + up_rows);
+    };
+#pragma unroll
+    for (int r = 0; r < kDepth - 1; ++r)
+      if (r < runs) fetch(x[r], xe[r], r);
+    if (runs) fetch_scales(0, b0);
+    if (b0 + 1 < b1) fetch_scales(1, b0 + 1);
 #pragma unroll 1
-    for (int b = b0; b < b1; ++b) {
-      const float s0 = s_gate, s1 = s_up;
-      float k0[2][4], k1[2][4];
+    for (int b = b0; b < b1; b += kDepth / 2) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int u = 0; u < kDepth / 2; ++u) {
+        if (b + u >= b1) break;
+        float k0[2][4], k1[2][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) k0[i][j] = k1[i][j] = 0.0f;
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        const int r = 2 * (b - b0) + c;
-        if (c == 0 || b + 1 < b1) fetch(x[1 - c], xe[1 - c], r + 1);
-        if (c == 1 && b + 1 < b1) {
-          s_gate = __ldg(S + b + 1);
-          s_up = __ldg(S + b + 1 + up_rows);
+          for (int j = 0; j < 4; ++j) k0[i][j] = k1[i][j] = 0.0f;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+          const int c = 2 * u + v, r = 2 * (b - b0) + c;
+          constexpr int kAhead = kDepth - 1;
+          if (r + kAhead < runs) fetch(x[(c + kAhead) % kDepth], xe[(c + kAhead) % kDepth], r + kAhead);
+          if (!kUp) {
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h) scale_hidden(x[c][h], xe[c][h], rexp[h]);
+          }
+          cp_async_wait<kStages - 2>();
+          mma_run<kWide>(k0, k1, ring + slot * kRunBytes, x[c][0], x[c][1]);
+          copy_run();                       // into the slot before this one, read by now
+          slot = slot + 1 == kStages ? 0 : slot + 1;
         }
-        if (!kUp) {
 #pragma unroll
-          for (int h = 0; h < kHalves; ++h) scale_hidden(x[c][h], xe[c][h], rexp[h]);
-        }
-        cp_async_wait<kStages - 2>();
-        mma_run<kWide>(k0, k1, ring + slot * kRunBytes, x[c][0], x[c][1]);
-        copy_run();                       // into the slot before this one, read by now
-        slot = slot + 1 == kStages ? 0 : slot + 1;
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            out[0][i][j] = fmaf(k0[i][j], i ? s_up[0] : s_gate[0], out[0][i][j]);
+            if (kWide) out[1][i][j] = fmaf(k1[i][j], i ? s_up[0] : s_gate[0], out[1][i][j]);
+          }
+        s_gate[0] = s_gate[1];
+        s_up[0] = s_up[1];
+        if (b + u + 2 < b1) fetch_scales(1, b + u + 2);
       }
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          out[0][i][j] = fmaf(k0[i][j], i ? s1 : s0, out[0][i][j]);
-          if (kWide) out[1][i][j] = fmaf(k1[i][j], i ? s1 : s0, out[1][i][j]);
-        }
     }
     if (sync) __syncthreads();
 #pragma unroll
