@@ -117,6 +117,19 @@ def test_all_tokens_on_one_expert(nb):
     verify(p, 1, got)
 
 
+def test_tokens_of_an_expert_in_several_units(nb):
+    """17 to 64 tokens of an expert are served by different CTAs, which all have to deal them out alike:
+    no token missed or taken twice, and every call the same to the bit."""
+    p, _ = layer(nb, 64, 512, 256, 8, shared=1, seed=7)
+    got = nb.fp8_moe(**p, top_k=4)
+    counts = torch.bincount(got[1].flatten().long(), minlength=8)
+    assert int(counts.max()) > 32 and int(counts.min()) > 8
+    verify(p, 4, got)
+    for _ in range(50):
+        again = nb.fp8_moe(**p, top_k=4)
+    assert all(torch.equal(u, v) for u, v in zip(got, again))
+
+
 def test_scales_of_the_operands(nb):
     """Rows of x far from 1, tiny and huge weights: the FP16 scaling must not overflow or vanish."""
     p, _ = layer(nb, 6, 128, 64, 3)
