@@ -2,6 +2,9 @@
 
     y = FP4(x) FP4(R)^T + sum_i alpha_i (x . v_i) u_i
 
+Beside it the layers of a model that stay at 8 bits: fp8_quant_act, fp8_pack_weight, fp8_gemm,
+block_norm and fp8_moe, in one FP8 block format.
+
 The compute is the C-ABI library libbiloco.so (include/biloco.h); this package
 is its thin ctypes binding.  Build the library with
 `python -m nvfp4_binary_rank_b200.build`.

@@ -443,8 +443,8 @@ __device__ __forceinline__ void scale_hidden(uint32_t (&v)[8], int2 e, int row_e
 // in distributed shared memory and there is no combine kernel.
 //
 // Measured, device time past L2: 64 tokens, 65 experts of 3 x 5120 x 2048 (2.05 GB): 414 us for
-// the layer, 4.9 TB/s of weights; 16 tokens, 32 + 1 experts of 3 x 4096 x 2048: 135 us, 5.4 TB/s.  Bound
-// by the latency of the loads: 16 warps an SM, each with 4 KB of weights on the way, leave the
+// the layer, 4.9 TB/s of weights; 16 tokens, 24 of 32 and one shared expert of 3 x 4096 x 2048
+// (0.63 GB): 134 us, 4.7 TB/s.  Bound by the latency of the loads: 16 warps an SM, each with 4 KB of weights on the way, leave the
 // schedulers idle for 60% of the time.  One token, 8 experts of 3 x 2048 x 1024: 26 us, of which 14 are
 // there without the weights, in the chain of three kernels: 5 us in the router (2.4 of them for
 // the choice), 3 and 2 us in the first pass of the products, about twice the time of a second

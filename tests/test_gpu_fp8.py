@@ -236,6 +236,18 @@ def test_gemm_parity_between_the_forms(nb, M, N, K, dtype):
     check(nb, xc, xs, wc, ws, nb.fp8_gemm(xc, xs, wc, ws, out_dtype=dtype))
 
 
+@pytest.mark.parametrize("M,N,K", [(100, 20000, 128), (70, 30000, 144), (128, 40000, 64), (33, 24000, 256)])
+def test_gemm_walks_over_small_tiles(nb, M, N, K):
+    """Short sums over many weight rows: more tiles of few columns than run at once."""
+    xc, xs, wc, ws = operands(nb, np.random.default_rng(N), M, N, K)
+    y = nb.fp8_gemm(xc, xs, wc, ws, out_dtype=torch.float32).double()
+    x = xc.double() * xs.t().repeat_interleave(128, 1)[:, :K].double()
+    w = wc.double() * ws.repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K].double()
+    S = x.abs() @ w.abs().t()
+    assert bool(((y - x @ w.t()).abs() <= (133 + -(-K // 128)) * 2.0 ** -23 * S).all())
+    assert nb.last_error() == 0
+
+
 @pytest.mark.parametrize("M,N", [(300, 2000), (130, 500), (70, 130)])
 def test_gemm_one_hot_rows_are_exact_in_wide_products(nb, M, N):
     K = 656
