@@ -93,24 +93,35 @@ __device__ __forceinline__ float max_abs(float a, uint64_t v) {
 }
 
 // Sum over the CTA; every thread gets it, summed in the same order.  `part` has one slot per
-// warp; its next use is a barrier later (the row's other sum, or the next row's).
-__device__ __forceinline__ float cta_sum(float v, float* part) {
+// warp, zeros behind them; its next use is a barrier later (the row's other sum, or the next row's).
+// Each thread adds up the slots itself: reads of shared memory at once, where shuffles
+// would be five dependent steps.
+template <int kSlots>
+__device__ __forceinline__ float cta_sum(float v, float4* part) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
   if (warps == 1) return v;
-  if (lane == 0) part[threadIdx.x >> 5] = v;
+  if (lane == 0) reinterpret_cast<float*>(part)[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = lane < warps ? part[lane] : 0.0f;
+  float4 s = part[0];
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-  return v;
+  for (int i = 1; i < kSlots / 4; ++i) {
+    if (4 * i >= warps) break;
+    const float4 q = part[i];
+    s.x += q.x;
+    s.y += q.y;
+    s.z += q.z;
+    s.w += q.w;
+  }
+  return (s.x + s.y) + (s.z + s.w);
 }
 
 template <int kVec, int kMaxThreads, bool kHf32, bool kWf32>
 __global__ void __launch_bounds__(kMaxThreads, kMaxThreads == 512 ? 2 : 1)
 block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
-  __shared__ float part[2][32];
+  constexpr int kSlots = kMaxThreads / 32;
+  __shared__ float4 part[2][kSlots / 4];
   const int D = a.D, nvec = D >> 3;
   constexpr int kHb = kHf32 ? 4 : 2;
   int at[kVec];                                // first element of this thread's pieces
@@ -135,6 +146,8 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
     }
   };
   griddep_launch_dependents();
+  if (threadIdx.x < 2 * kSlots) reinterpret_cast<float*>(part)[threadIdx.x] = 0.0f;
+  __syncthreads();
   griddep_wait();
   load_row(static_cast<int>(blockIdx.x));
   const float inv_d = 1.0f / static_cast<float>(D);
@@ -151,7 +164,7 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
           const uint64_t v = y[i].pair(j);
           ss = f32x2_fma(v, v, ss);
         }
-      post = both(rsqrtf(cta_sum(f32x2_sum(ss), part[0]) * inv_d + a.eps));
+      post = both(rsqrtf(cta_sum<kSlots>(f32x2_sum(ss), part[0]) * inv_d + a.eps));
     }
     uint64_t r[kVec][4], ss = 0;
 #pragma unroll
@@ -202,7 +215,7 @@ block_norm_kernel(const __grid_constant__ BlockNormArgs a) {
       if (a.post_w) __syncthreads();      // the one sum of this row is read before the next row's is written
       continue;
     }
-    const uint64_t pre = both(rsqrtf(cta_sum(f32x2_sum(ss), part[1]) * inv_d + a.eps));
+    const uint64_t pre = both(rsqrtf(cta_sum<kSlots>(f32x2_sum(ss), part[1]) * inv_d + a.eps));
     float top[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
