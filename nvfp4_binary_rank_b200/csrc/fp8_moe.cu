@@ -442,8 +442,8 @@ __device__ __forceinline__ void scale_hidden(uint32_t (&v)[8], int2 e, int row_e
 // kOne (down, one token): a cluster of the token's experts owns 64 output rows; the shares meet
 // in distributed shared memory and there is no combine kernel.
 //
-// Measured, device time past L2: 64 tokens, 65 experts of 3 x 5120 x 2048 (2.05 GB): 414 us for
-// the layer, 4.9 TB/s of weights; 16 tokens, 24 of 32 and one shared expert of 3 x 4096 x 2048
+// Measured, device time past L2: 64 tokens, 65 experts of 3 x 5120 x 2048 (2.05 GB): 409 us for
+// the layer, 5.0 TB/s of weights; 16 tokens, 24 of 32 and one shared expert of 3 x 4096 x 2048
 // (0.63 GB): 134 us, 4.7 TB/s.  Bound by the latency of the loads: 16 warps an SM, each with 4 KB of weights on the way, leave the
 // schedulers idle for 60% of the time.  One token, 8 experts of 3 x 2048 x 1024: 26 us, of which 14 are
 // there without the weights, in the chain of three kernels: 5 us in the router (2.4 of them for
@@ -803,8 +803,8 @@ cudaError_t launch_fp8_moe(MoeArgs& a, cudaStream_t s) {
     };
     raise(moe_route_kernel<1, false>, BILOCO_MOE_MAX_D * 2);
     raise(moe_route_kernel<1, true>, BILOCO_MOE_MAX_D * 2);
-    raise(moe_route_kernel<4, false>, 4 * BILOCO_MOE_MAX_D * 2);
-    raise(moe_route_kernel<4, true>, 4 * BILOCO_MOE_MAX_D * 2);
+    raise(moe_route_kernel<2, false>, 2 * BILOCO_MOE_MAX_D * 2);
+    raise(moe_route_kernel<2, true>, 2 * BILOCO_MOE_MAX_D * 2);
     raise(moe_product_kernel<true, 8>, kStreamBytes);
     raise(moe_product_kernel<true, 4>, kStreamBytes);
     raise(moe_product_kernel<true, 2>, kStreamBytes);
@@ -815,16 +815,18 @@ cudaError_t launch_fp8_moe(MoeArgs& a, cudaStream_t s) {
   });
   if (d.err != cudaSuccess) return d.err;
 
-  // up to 16 tokens a cluster each (128 CTAs); above, four tokens share a cluster's reads of the router
-  const int tok = a.T <= 16 ? 1 : 4;
+  // Up to 32 tokens a cluster each; above, two share a cluster's reads of the router.  Measured, us of
+  // a layer with little else to do (F = 16) with 1, 2, 4 tokens a cluster: 37, 39, 42 (16 x 4096, 64
+  // experts), 44, 46, 51 (32 x 4096), 66, 64, 68 (64 x 5120), 96, 92, 96 (64 x 2048, 512 experts).
+  const int tok = a.T <= 32 ? 1 : 2;
   const unsigned grid = static_cast<unsigned>((a.T + tok - 1) / tok * kRouteCtas);
   const size_t sm = static_cast<size_t>(tok) * a.D * 2;
   if (tok == 1)
     e = a.router_f32 ? launch_pdl(moe_route_kernel<1, true>, grid, kThreads, sm, kRouteCtas, s, a)
                      : launch_pdl(moe_route_kernel<1, false>, grid, kThreads, sm, kRouteCtas, s, a);
   else
-    e = a.router_f32 ? launch_pdl(moe_route_kernel<4, true>, grid, kThreads, sm, kRouteCtas, s, a)
-                     : launch_pdl(moe_route_kernel<4, false>, grid, kThreads, sm, kRouteCtas, s, a);
+    e = a.router_f32 ? launch_pdl(moe_route_kernel<2, true>, grid, kThreads, sm, kRouteCtas, s, a)
+                     : launch_pdl(moe_route_kernel<2, false>, grid, kThreads, sm, kRouteCtas, s, a);
   if (e != cudaSuccess) return e;
 
   const int units = std::min(a.T * a.k, a.E) + a.shared * ((a.T + 15) / 16);     // about
