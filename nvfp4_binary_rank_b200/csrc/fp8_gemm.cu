@@ -9,7 +9,7 @@
 // FP32; y is rounded once.
 //
 // Two forms of one kernel:
-//   rows form (more than 128 tokens): the MMA's rows are tokens and its columns weight
+//   rows form (more than 128 tokens, larger products): the MMA's rows are tokens and its columns weight
 //     rows, so a thread's scale is one number per block (its token's times its 128
 //     columns').  A pair of CTAs (cta_group::2) computes 256 tokens x 256 weight rows, each
 //     CTA loading 128 rows of either operand: 32 KB per block and SM instead of 48.
@@ -18,7 +18,7 @@
 //     its columns tokens, so a decode batch is not padded to 128 rows; scales vary over the
 //     columns.  Bound by reading the weight.
 // Measured, device time past L2 (M tokens, N x K weight):
-//   4096, 13824 x 5120: 268 us, 2.16 PFLOP/s.  A block of 128 takes about 790 clocks, of which its
+//   4096, 13824 x 5120: 265 us, 2.19 PFLOP/s.  A block of 128 takes about 790 clocks, of which its
 //     MMAs are 513; the rest is the chain commit - read back - release of an accumulator.  Runs
 //     of seconds are held by the power limit at about 310 us.
 //   512, 5120 x 5120: 23.5 us;  333, 1000 x 2064: 9.2 us (latency of one chain of blocks)

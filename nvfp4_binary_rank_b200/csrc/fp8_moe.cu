@@ -444,12 +444,13 @@ __device__ __forceinline__ void scale_hidden(uint32_t (&v)[8], int2 e, int row_e
 //
 // Measured, device time past L2: 64 tokens, 65 experts of 3 x 5120 x 2048 (2.05 GB): 409 us for
 // the layer, 5.0 TB/s of weights; 16 tokens, 24 of 32 and one shared expert of 3 x 4096 x 2048
-// (0.63 GB): 134 us, 4.7 TB/s.  Bound by the latency of the loads: 16 warps an SM, each with 4 KB of weights on the way, leave the
-// schedulers idle for 60% of the time.  One token, 8 experts of 3 x 2048 x 1024: 26 us, of which 14 are
-// there without the weights, in the chain of three kernels: 5 us in the router (2.4 of them for
-// the choice), 3 and 2 us in the first pass of the products, about twice the time of a second
-// one, since its instructions come from L2.  Passes without tokens while the kernel before runs, to
-// have the instructions, won 1 us there and cost 20 at 64 tokens.
+// (0.63 GB): 134 us, 4.7 TB/s.  Bound by the latency of the loads: 16 warps an SM, each with 4 KB
+// of weights on the way, leave the schedulers idle for 60% of the time.  One token, 8 experts of
+// 3 x 2048 x 1024: 26 us, of which 14 are there without the weights, in the chain of three kernels:
+// 5 us in the router (2.4 of them for the choice), 3 and 2 us in the first pass of the products,
+// about twice the time of a second one, since its instructions come from L2.  Passes without
+// tokens while the kernel before runs, to have the instructions, won 1 us there and cost 20 at 64
+// tokens.
 template <bool kUp, int kSplit, bool kOne = false>
 __global__ void __launch_bounds__(kThreads, 2)
 moe_product_kernel(const __grid_constant__ MoeArgs a) {
