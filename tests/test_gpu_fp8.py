@@ -290,6 +290,23 @@ def test_gemm_many_calls_of_both_forms_in_a_row(nb):
     assert nb.last_error() == 0
 
 
+@pytest.mark.parametrize("M", [1, 400])
+def test_a_weight_packed_just_before_its_product(nb, M):
+    """The product requests its weight early; a packer right in front of it has to come first all the same."""
+    N, K = 2048, 2064
+    x = nb.fp8_quant_act(activation(np.random.default_rng(13), M, K))
+    ws = [torch.randn((N, K), generator=torch.Generator().manual_seed(i)).cuda() for i in range(3)]
+    want = []
+    for w in ws:
+        packed = nb.fp8_pack_weight(w)
+        torch.cuda.synchronize()
+        want.append(nb.fp8_gemm(*x, *packed))
+        torch.cuda.synchronize()
+    del packed
+    for i in range(150):                     # the same memory for every packed weight
+        assert torch.equal(nb.fp8_gemm(*x, *nb.fp8_pack_weight(ws[i % 3])), want[i % 3])
+
+
 @pytest.mark.parametrize("M", [1, 50, 400])
 def test_streams_and_graphs(nb, M):
     """Two calls at once on two streams, and a captured quantise + product replayed on new inputs."""

@@ -183,6 +183,77 @@ def test_strided_rows_streams_and_graphs(nb):
     assert all(torch.equal(u, v) for _, o in graphs for u, v in zip(want, o))
 
 
+@pytest.mark.parametrize("T,k,shared", [(1, 3, 1), (40, 3, 1), (1, 8, 1)])
+def test_two_streams_and_two_graphs_at_once(nb, T, k, shared):
+    """One token (clusters of its experts, with and without the combine kernel) and units of 16."""
+    p, _ = layer(nb, T, 272, 80, 8, shared)
+    q, _ = layer(nb, T, 272, 80, 8, shared, seed=5)
+    want, other = nb.fp8_moe(**p, top_k=k), nb.fp8_moe(**q, top_k=k)
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(50):
+        a, b = nb.fp8_moe(**p, top_k=k, stream=s1), nb.fp8_moe(**q, top_k=k, stream=s2)
+    torch.cuda.synchronize()
+    assert all(torch.equal(u, v) for u, v in zip(want, a)) and all(torch.equal(u, v) for u, v in zip(other, b))
+    graphs = []
+    for w in (p, q):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = nb.fp8_moe(**w, top_k=k)
+        graphs.append((g, out))
+    for _ in range(20):
+        for (g, _), s in zip(graphs, (s1, s2)):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for (_, out), w in zip(graphs, (want, other)):
+        assert all(torch.equal(u, v) for u, v in zip(out, w))
+
+
+@pytest.mark.parametrize("T", [1, 33])
+def test_a_bias_of_minus_infinity_leaves_an_expert_out(nb, T):
+    """Masked experts are picked only where nothing else is left, and then the lowest first."""
+    p, _ = layer(nb, T, 128, 64, 40)
+    b = torch.full((40,), float("-inf"), device="cuda")
+    b[[7, 31]] = torch.tensor([0.25, -3.0], device="cuda")
+    for score in ("softmax", "sigmoid"):
+        got = nb.fp8_moe(**p, top_k=4, bias=b, score=score)
+        assert got[1].tolist() == [[7, 31, 0, 1]] * T
+        verify(p, 4, got, bias=b, score=score)
+
+
+@pytest.mark.parametrize("T", [1, 17])
+def test_the_largest_sizes(nb, T):
+    """D and F at their limit; the formula and the tolerance in FP64 on the GPU."""
+    D = F = 16384
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn((T, D), generator=g, device="cuda").to(torch.bfloat16)
+    router = (torch.randn((2, D), generator=g, device="cuda") * 0.05).to(torch.bfloat16)
+    w13, s13 = nb.fp8_pack_weight((torch.randn((2, 2 * F, D), generator=g, device="cuda") * 0.02).to(torch.bfloat16))
+    w2, s2 = nb.fp8_pack_weight((torch.randn((2, D, F), generator=g, device="cuda") * 0.02).to(torch.bfloat16))
+    y, ids, w = nb.fp8_moe(x, router, w13, s13, w2, s2, 1)
+    assert torch.equal(ids[:, 0].long(), (x.double() @ router.double().t()).argmax(1)) and bool((w == 1).all())
+
+    def wide(c, s):
+        return c.double() * s.double().repeat_interleave(128, 0).repeat_interleave(128, 1)
+
+    c = (136 + 128 + 80) * 2.0 ** -23
+    for e in range(2):
+        t = (ids[:, 0] == e).nonzero()[:, 0]
+        if len(t) == 0:
+            continue
+        W, xe = wide(w13[e], s13[e]), x[t].double()
+        a, ax = xe @ W.t(), xe.abs() @ W.abs().t()
+        del W
+        sg, u = torch.nn.functional.silu(a[:, :F]), a[:, F:]
+        h = sg * u
+        dh = 1.1 * u.abs() * c * ax[:, :F] + sg.abs() * c * ax[:, F:] + (2.0 ** -20 + 2.0 ** -11) * h.abs()
+        dh += 2.0 ** -25 * h.abs().view(len(t), -1, 16).amax(2).repeat_interleave(16, 1) + 2.0 ** -38 * h.abs().max()
+        V = wide(w2[e], s2[e])
+        want, tol = h @ V.t(), (dh + c * h.abs()) @ V.abs().t()
+        assert bool(((y[t].double() - want).abs() <= (tol + 2.0 ** -8 * want.abs()) * (1 + 2.0 ** -7)).all())
+
+
 def test_empty_and_refusals(nb):
     p, _ = layer(nb, 2, 64, 32, 4)
     y, ids, w = nb.fp8_moe(**{**p, "x": p["x"][:0]}, top_k=2)
