@@ -567,9 +567,20 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
       for (int j = 0; j < C::kCols / 2; ++j)
         asm("mov.b64 {%0, %1}, %2;" : "=f"(v[2 * j]), "=f"(v[2 * j + 1]) : "l"(acc[j]));
       if (p.split > 1) {
-        // every product of this CTA's part is done: the stages are free for the exchange
+        // The sums go into the stages, which every product of this CTA's part has to have read
+        // first.  The rows form's second half of a block comes after its first, so the groups of the
+        // first half wait for it too: for the last block, behind which its barrier is not used again.
+        if (!kSwap && ok) {
+          const int last = (k1 - k0 - 1) % C::kStages, lphase = (k1 - k0 - 1) / C::kStages & 1;
+          if (__any_sync(0xFFFFFFFFu, !mbar_wait(freed0 + 8 * last, lphase, stop))) {
+            ok = false;
+            give_up();
+          }
+        }
         float* x = reinterpret_cast<float*>(smem_raw + (smem - smem_u32(smem_raw)));
-        if (kSwap) {
+        if (!ok) {
+          // products may still be under way: the stages stay as they are, y is not written
+        } else if (kSwap) {
 #pragma unroll
           for (int j = 0; j < C::kCols; ++j) x[(grp * C::kCols + j) * C::kPitch + row] = v[j];
         } else {

@@ -192,6 +192,29 @@ def test_gemm_many_calls_in_a_row(nb):
     assert nb.last_error() == 0
 
 
+@pytest.mark.parametrize("M,N,K", [(129, 5120, 5120), (256, 5120, 5120), (257, 2048, 4096), (192, 5120, 13824),
+                                   (130, 5200, 1040)])
+def test_gemm_parts_of_k_in_the_rows_form_repeat_to_the_bit(nb, M, N, K):
+    """The rows form with K split into parts of 3 to 36 blocks: the parts' sums take the place of the
+    operands, which both halves of a tile's columns must have been multiplied from.  Against an FP64
+    product, then the same bits in a thousand calls, alone and with another product under way."""
+    xc, xs, wc, ws = operands(nb, np.random.default_rng(M + N + K), M, N, K)
+    y = nb.fp8_gemm(xc, xs, wc, ws, out_dtype=torch.float32)
+    x = xc.double() * xs.t().repeat_interleave(128, 1)[:, :K].double()
+    w = wc.double() * ws.repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K].double()
+    S = x.abs() @ w.abs().t()
+    assert bool(((y.double() - x @ w.t()).abs() <= (133 + -(-K // 128)) * 2.0 ** -23 * S).all())
+    other, s = operands(nb, np.random.default_rng(1), 200, 1024, 2064), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(1000):
+        if i % 2:
+            nb.fp8_gemm(*other, stream=s)
+        differ += (nb.fp8_gemm(xc, xs, wc, ws, out_dtype=torch.float32) != y).sum()
+    assert int(differ) == 0
+    assert nb.last_error() == 0
+
+
 def test_gemm_out_argument_and_neighbours_untouched(nb):
     M, N, K = 5, 100, 144
     xc, xs, wc, ws = operands(nb, np.random.default_rng(6), M, N, K)
