@@ -78,7 +78,7 @@ __device__ __forceinline__ uint32_t f16x2_from_e4m3x2(uint32_t codes) {
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 
 // Exponent e with 2^e <= |largest| < 2^(e+1), from the FP32 bits of a maximum; kept where
-// 2^-e, 2^(14 - e) and 2^(e - 14) are normal numbers.
+// 2^(1 - e), 2^(14 - e) and 2^(e - 14) are normal numbers (2^-127 is not).
 __device__ __forceinline__ int exponent_of(uint32_t bits) {
   return min(max(static_cast<int>(bits >> 23) - 127, -100), 127);
 }
@@ -643,7 +643,8 @@ moe_product_kernel(const __grid_constant__ MoeArgs a) {
             const int ex = exponent_of(m), f = (grp0 + grp) * 16 + i * 8;
             top = max(top, m);
             if (r < cnt) {
-              a.h[static_cast<long long>(q) * F + f + g] = static_cast<uint16_t>(f16x2_from_f32(v * pow2(-ex), 0.0f));
+              a.h[static_cast<long long>(q) * F + f + g] =
+                  static_cast<uint16_t>(f16x2_from_f32(0.5f * v * pow2(1 - ex), 0.0f));
               if (g == 0) a.hexp[static_cast<long long>(q) * (F / 8) + f / 8] = ex;
             }
           }

@@ -141,6 +141,32 @@ def test_scales_of_the_operands(nb):
     assert bool((nb.fp8_moe(**p, top_k=2)[0][4] == 0).all())
 
 
+@pytest.mark.parametrize("T", [1, 20])
+def test_hidden_values_up_to_the_largest_float(nb, T):
+    """Gate and up of about 2^63 each: hidden values from 2^126 to 2^127.8 stay in the sum, and an
+    infinite one spoils its own token only."""
+    D = F = 128
+    rng = np.random.default_rng(T)
+    p, _ = layer(nb, T, D, F, 3)
+    codes = rng.integers(0x38, 0x40, (3, 2 * F, D)).astype(np.uint8)               # 1 to 1.875
+    codes[:, F:] |= rng.integers(0, 2, (3, F, D)).astype(np.uint8) << 7
+    p["w13"] = torch.from_numpy(codes).cuda().view(torch.float8_e4m3fn)
+    p["w13_scales"] = torch.full((3, 2, 1), 2.0 ** 63, device="cuda")
+    p["w2_scales"] = p["w2_scales"] * 2.0 ** -110
+    x = torch.zeros((T, D))
+    x[torch.arange(T), torch.from_numpy(rng.permutation(D)[:T])] = torch.tensor([1.0, 0.5, 2.0 ** -50, 1.0])[torch.arange(T) % 4]
+    p["x"] = x.to(torch.bfloat16).cuda()
+    got = nb.fp8_moe(**p, top_k=2)
+    W = dequant(p["w13"], p["w13_scales"])[got[1][0, 0].item()] @ x[0].double().numpy()
+    assert (np.abs(W[:F] * W[F:]) >= 2.0 ** 127).sum() > 20                        # the case is what it says
+    verify(p, 2, got)
+    if T > 1:
+        p["x"][3] *= 4
+        y = nb.fp8_moe(**p, top_k=2)[0]
+        keep = [t for t in range(T) if t != 3]
+        assert torch.equal(y[keep], got[0][keep]) and not bool(y[3].isfinite().all())
+
+
 def test_a_bad_token_spoils_only_its_row(nb):
     p, _ = layer(nb, 20, 144, 48, 4)
     clean, ids, _ = nb.fp8_moe(**p, top_k=2)
