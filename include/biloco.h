@@ -463,6 +463,14 @@ int biloco_selftest_wait_timeout(biloco_stream_t stream);
  */
 int biloco_selftest_drop_arrivals(int mask);
 
+/*
+ * biloco_selftest_drop_scales - the same for biloco_fp8_gemm: in its next call that has
+ * rows the block scales never arrive.  The kernel gives up after its bounded wait (about
+ * 1 s, and at most another until its last product has ended) and records
+ * BILOCO_ERR_TIMEOUT; y of that call is not valid.
+ */
+int biloco_selftest_drop_scales(void);
+
 /* Human-readable name of a status code (static storage). */
 const char *biloco_status_string(int status);
 

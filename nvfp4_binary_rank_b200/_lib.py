@@ -54,6 +54,7 @@ SIGNATURES = {
     "biloco_last_error": (_I, [_P]),
     "biloco_selftest_wait_timeout": (_I, [_P]),
     "biloco_selftest_drop_arrivals": (_I, [_I]),
+    "biloco_selftest_drop_scales": (_I, []),
     "biloco_set_launch": (_I, [_I]),
     "biloco_get_launch": (_I, []),
     "biloco_set_correction": (_I, [_I]),
@@ -239,6 +240,12 @@ def selftest_drop_arrivals(mask: int):
     (1: z slices, 2: activation image); its bounded waits expire after about 1 s
     and biloco_last_error then reports BILOCO_ERR_TIMEOUT."""
     _check("biloco_selftest_drop_arrivals", load().biloco_selftest_drop_arrivals(int(mask)))
+
+
+def selftest_drop_scales():
+    """Make the block scales of the next fp8_gemm call (with at least one row) never arrive; its bounded
+    waits expire after about 1 s and biloco_last_error then reports BILOCO_ERR_TIMEOUT."""
+    _check("biloco_selftest_drop_scales", load().biloco_selftest_drop_scales())
 
 
 def set_launch(flags: int):

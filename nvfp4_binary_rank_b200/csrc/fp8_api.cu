@@ -63,6 +63,11 @@ int biloco_fp8_gemm(const uint8_t* x_codes, const float* x_scales, const uint8_t
                       reinterpret_cast<cudaStream_t>(stream));
 }
 
+int biloco_selftest_drop_scales(void) {
+  fp8_drop_scales();
+  return BILOCO_OK;
+}
+
 int biloco_block_norm(const void* y_bf16, long long ldy, const void* h, long long ldh, int h_type,
                       const void* post_weight, const void* pre_weight, int w_type, const void* gate, int gate_type,
                       int gate_rows, float res_scale, float offset, float eps, int M, int D, void* h_out,

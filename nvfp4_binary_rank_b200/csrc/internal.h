@@ -45,6 +45,8 @@ bool make_tmap(CUtensorMap* m, const void* base, uint64_t inner_bytes, uint64_t 
 
 // Status word of the FP8 GEMM on the current device: read on `s`, returned and cleared (synchronous).
 int fp8_take_status(cudaStream_t s);
+// The next FP8 GEMM call leaves out its scales' arrivals (failure-path self test).
+void fp8_drop_scales();
 
 // Launchers (return cudaError_t values).
 cudaError_t launch_quant_act_rowmajor(const uint16_t* x, int M, int K, uint8_t* codes, uint8_t* sf,

@@ -80,6 +80,28 @@ def test_dropped_arrivals_expire_inside_the_gemm(nb, entry, mask, M, N, K):
     np.testing.assert_array_equal(y_to_numpy(y2), y_to_numpy(y0))
 
 
+# swapped form: one tile a cluster of 8 parts, tiles of 32 to 128 columns, several tiles a CTA; rows form: K split
+# over pairs, one tile a pair, several tiles a pair
+@pytest.mark.timeout(120, method="thread")
+@pytest.mark.parametrize("M,N,K", [(1, 512, 5120), (40, 1000, 2064), (60, 5120, 1024), (128, 5120, 5120), (3, 60000, 1024),
+                                   (129, 5120, 5120), (333, 1800, 2064), (2048, 5120, 1024)])
+def test_scales_that_never_arrive_expire_inside_the_fp8_product(nb, M, N, K):
+    g = torch.Generator().manual_seed(M)
+    w = nb.fp8_pack_weight(torch.randn((N, K), generator=g).cuda())
+    x = nb.fp8_quant_act(torch.randn((M, K), generator=g).to(torch.bfloat16).cuda())
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    y0 = nb.fp8_gemm(*x, *w, stream=s)                    # a correct call first
+    assert nb.last_error(s) == 0
+    nb.selftest_drop_scales()
+    nb.fp8_gemm(*x, *w, stream=s)                         # its waits expire after ~1 s
+    assert nb.last_error(s) == nb._lib.ERR_TIMEOUT
+    assert nb.last_error(s) == 0
+    y1, y2 = nb.fp8_gemm(*x, *w, stream=s), nb.fp8_gemm(*x, *w, stream=s)
+    assert nb.last_error(s) == 0
+    assert torch.equal(y0, y1) and torch.equal(y0, y2)
+
+
 def test_drop_request_is_consumed_by_one_call(nb):
     # a request made before a call that does not take the decode kernel (here the
     # local-z schedule, which runs the general kernel) is consumed by that call and
