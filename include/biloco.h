@@ -309,8 +309,10 @@ int biloco_fp8_pack_weight(const void *W, int w_type, int E, int N, int K, uint8
  * other.  Sums are FP32; the result depends only on the operands and the shape.
  * The kernel is launched with programmatic dependent launch and reads w_codes before it
  * waits for the kernel before it (see biloco_gemm on what must not write the weight).
- * A bounded wait that expires inside the kernel is reported by biloco_last_error, on
- * whichever stream asks first; y is then not valid.
+ * A bounded wait that expires inside the kernel is reported by biloco_last_error on the
+ * call's stream; y is then not valid.  That of a call captured into a graph, or on a
+ * stream beyond the first 1023 that made such calls on the device, is reported on whichever
+ * stream asks first.
  */
 int biloco_fp8_gemm(const uint8_t *x_codes, const float *x_scales, const uint8_t *w_codes,
                     const float *w_scales, void *y, int y_type, int M, int N, int K,
@@ -432,7 +434,8 @@ int biloco_resolve_mode(int M, int N, int K, int r);
  * checked and reset the same way; because that array serves every stream, the
  * call then synchronises the whole device first (cudaDeviceSynchronize), so that
  * a no-allocation call still running on another stream is neither missed nor
- * cleared while it runs.
+ * cleared while it runs.  The same holds once a biloco_fp8_gemm call has been captured into
+ * a graph.  Where several calls recorded errors, the FP8 product's are kept for the next ask.
  */
 int biloco_last_error(biloco_stream_t stream);
 

@@ -312,8 +312,8 @@ int biloco_last_error(biloco_stream_t stream) {
     }
   }
   const int static_status = noalloc_take_status();
-  const int fp8_status = fp8_take_status(s);
-  return status != 0 ? status : static_status != 0 ? static_status : fp8_status;
+  if (status != 0 || static_status != 0) return status != 0 ? status : static_status;
+  return fp8_take_status(s);
 }
 
 const char* biloco_status_string(int status) {

@@ -40,7 +40,9 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <map>
 #include <mutex>
+#include <utility>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -55,7 +57,10 @@ namespace biloco {
 
 namespace {
 
-__device__ int g_fp8_status;     // first device-side error of an FP8 GEMM on this device
+// First device-side error of a stream's FP8 GEMMs, a word for each stream.  Word 0 is that of calls
+// captured into graphs, which any stream may replay, and of streams that found no word left.
+constexpr int kStatusWords = 1024;
+__device__ int g_fp8_status[kStatusWords];
 
 struct Fp8GemmParams {
   const float* xs;       // [KB][M]
@@ -65,6 +70,7 @@ struct Fp8GemmParams {
   int tiles_a, tiles_b;  // tiles along the MMA's rows and columns
   int split;             // CTAs of the cluster that splits K
   int y_f32;
+  int status_word;
   int drop;              // failure-path self test: the scales never arrive
   int vec;               // bytes of the widest aligned store of a y row: 32, 16, 8 or 2
 };
@@ -308,7 +314,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
   volatile int* const stop = &abort_flag;
   auto give_up = [&] {
     *stop = 1;
-    record_error(&g_fp8_status, kDevErrTimeout);
+    record_error(&g_fp8_status[p.status_word], kDevErrTimeout);
   };
 
   // Rows form: the promoting warps take registers from the others.  Nobody takes any back
@@ -663,6 +669,46 @@ constexpr int kMaxDevices = 64;
 
 std::atomic<bool> g_drop_scales{false};   // failure-path self test, consumed by the next product
 
+// The status words handed out, by device.
+struct StatusWords {
+  std::mutex mu;
+  std::map<std::pair<int, cudaStream_t>, int> of_stream;
+  int next[kMaxDevices] = {};
+  bool shared[kMaxDevices] = {};         // word 0 may hold something
+};
+StatusWords g_words;
+
+// The word for a call on stream `s` of the current device `dev`; -1 where CUDA refuses.
+int status_word(int dev, cudaStream_t s) {
+  cudaStreamCaptureStatus capture;
+  if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) return -1;
+  std::lock_guard<std::mutex> lk(g_words.mu);
+  if (capture == cudaStreamCaptureStatusNone) {
+    const auto at = g_words.of_stream.find({dev, s});
+    if (at != g_words.of_stream.end()) return at->second;
+    if (g_words.next[dev] + 1 < kStatusWords) return g_words.of_stream[{dev, s}] = ++g_words.next[dev];
+  }
+  g_words.shared[dev] = true;
+  return 0;
+}
+
+// Reads and clears a word on `s`.
+int take_word(int word, cudaStream_t s) {
+  int status = 0;
+  if (cudaMemcpyFromSymbolAsync(&status, g_fp8_status, sizeof(int), word * sizeof(int), cudaMemcpyDeviceToHost, s) !=
+          cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return BILOCO_ERR_CUDA;
+  if (status != 0) {
+    const int zero = 0;
+    if (cudaMemcpyToSymbolAsync(g_fp8_status, &zero, sizeof(int), word * sizeof(int), cudaMemcpyHostToDevice, s) !=
+            cudaSuccess ||
+        cudaStreamSynchronize(s) != cudaSuccess)
+      return BILOCO_ERR_CUDA;
+  }
+  return status;
+}
+
 template <bool kSwap, int kBN>
 cudaError_t launch_instance(const CUtensorMap& ta, const CUtensorMap& tb, Fp8GemmParams& p, cudaStream_t s) {
   using C = Cfg<kSwap, kBN>;
@@ -721,17 +767,22 @@ cudaError_t launch_instance(const CUtensorMap& ta, const CUtensorMap& tb, Fp8Gem
 void fp8_drop_scales() { g_drop_scales.store(true); }
 
 int fp8_take_status(cudaStream_t s) {
-  int status = 0;
-  if (cudaMemcpyFromSymbolAsync(&status, g_fp8_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-      cudaStreamSynchronize(s) != cudaSuccess)
-    return BILOCO_ERR_CUDA;
-  if (status != 0) {
-    const int zero = 0;
-    if (cudaMemcpyToSymbolAsync(g_fp8_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
-        cudaStreamSynchronize(s) != cudaSuccess)
-      return BILOCO_ERR_CUDA;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return BILOCO_ERR_CUDA;
+  if (dev >= kMaxDevices) return BILOCO_OK;
+  int own = 0;
+  bool shared = false;
+  {
+    std::lock_guard<std::mutex> lk(g_words.mu);
+    const auto at = g_words.of_stream.find({dev, s});
+    if (at != g_words.of_stream.end()) own = at->second;
+    shared = g_words.shared[dev];
   }
-  return status;
+  const int status = own ? take_word(own, s) : BILOCO_OK;
+  if (status != BILOCO_OK || !shared) return status;
+  // any stream's kernels may write word 0: wait for all of them, so that nothing is missed or cleared early
+  if (cudaDeviceSynchronize() != cudaSuccess) return BILOCO_ERR_CUDA;
+  return take_word(0, s);
 }
 
 // Columns of the swapped form's tiles.  Up to 32 tokens one tile takes all.  Above, small tiles
@@ -773,6 +824,10 @@ int run_fp8_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const fl
   p.KB = (K + kFp8Block - 1) / kFp8Block;
   p.NB = (N + 127) / 128;
   p.y_f32 = y_f32;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return BILOCO_ERR_CUDA;
+  p.status_word = status_word(dev, s);
+  if (p.status_word < 0) return BILOCO_ERR_CUDA;
   p.drop = g_drop_scales.exchange(false);
   const unsigned long long bits = reinterpret_cast<uintptr_t>(y) | static_cast<unsigned long long>(N) * (y_f32 ? 4 : 2);
   p.vec = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : 2;

@@ -43,7 +43,7 @@ int check_device();
 // Tensor map of a 2-D byte tensor [rows][inner_bytes], box [box_rows][128 B], 128-byte swizzle.
 bool make_tmap(CUtensorMap* m, const void* base, uint64_t inner_bytes, uint64_t rows, uint32_t box_rows);
 
-// Status word of the FP8 GEMM on the current device: read on `s`, returned and cleared (synchronous).
+// Status of the FP8 GEMMs on `s` of the current device, else of captured ones: returned and cleared (synchronous).
 int fp8_take_status(cudaStream_t s);
 // The next FP8 GEMM call leaves out its scales' arrivals (failure-path self test).
 void fp8_drop_scales();

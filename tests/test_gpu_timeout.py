@@ -102,6 +102,60 @@ def test_scales_that_never_arrive_expire_inside_the_fp8_product(nb, M, N, K):
     assert torch.equal(y0, y1) and torch.equal(y0, y2)
 
 
+def expire(nb, s, M=3, N=256, K=1024):
+    x = nb.fp8_quant_act(torch.ones((M, K), dtype=torch.bfloat16, device="cuda"))
+    w = nb.fp8_pack_weight(torch.ones((N, K), device="cuda"))
+    torch.cuda.synchronize()
+    nb.selftest_drop_scales()
+    nb.fp8_gemm(*x, *w, stream=s)
+    return x, w
+
+
+def test_an_expired_fp8_product_is_its_own_streams_error(nb):
+    """Other streams, asked before and after the kernel has given up, report nothing and clear nothing."""
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    nb.last_error(a)
+    x, w = expire(nb, a)
+    y = nb.fp8_gemm(*x, *w, stream=b)
+    assert nb.last_error(b) == 0                           # the other stream's kernel still waits
+    a.synchronize()
+    assert nb.last_error(b) == 0 and nb.last_error() == 0
+    assert nb.last_error(a) == nb._lib.ERR_TIMEOUT
+    assert nb.last_error(a) == 0
+    assert torch.equal(y, nb.fp8_gemm(*x, *w))
+    # two streams, each its own
+    expire(nb, a)
+    expire(nb, b)
+    assert nb.last_error(b) == nb._lib.ERR_TIMEOUT and nb.last_error() == 0
+    assert nb.last_error(a) == nb._lib.ERR_TIMEOUT
+    assert nb.last_error(a) == 0 and nb.last_error(b) == 0
+
+
+def test_an_expired_fp8_product_in_a_graph_is_reported(nb):
+    """A captured product may be replayed on any stream: whichever asks first is told, once."""
+    x = nb.fp8_quant_act(torch.ones((3, 1024), dtype=torch.bfloat16, device="cuda"))
+    w = nb.fp8_pack_weight(torch.ones((256, 1024), device="cuda"))
+    want = nb.fp8_gemm(*x, *w)
+    graphs = []
+    for drop in (True, False):
+        if drop:
+            nb.selftest_drop_scales()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            y = nb.fp8_gemm(*x, *w)
+        graphs.append((g, y))
+    s, other = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        graphs[0][0].replay()
+    assert nb.last_error(other) == nb._lib.ERR_TIMEOUT    # it waited for the replay
+    assert nb.last_error(s) == 0 and nb.last_error() == 0
+    with torch.cuda.stream(s):
+        graphs[1][0].replay()
+    assert nb.last_error(s) == 0
+    assert torch.equal(graphs[1][1], want)
+
+
 def test_drop_request_is_consumed_by_one_call(nb):
     # a request made before a call that does not take the decode kernel (here the
     # local-z schedule, which runs the general kernel) is consumed by that call and
