@@ -7,10 +7,14 @@ A decode step calls these once per layer with microseconds of GPU work, so a pla
 (contiguous operands, the current device and stream) goes through _binding.so, which checks
 it, allocates its outputs and calls the library.  What that does not take comes back as None
 and is checked here: strided rows, another stream or device, an output to write into, and
-every call that is refused.
+every call that is refused.  Where _binding.so is missing or was built for another PyTorch, every
+call is made from here, after one warning.
 """
 
 from __future__ import annotations
+
+import importlib
+import warnings
 
 import torch
 
@@ -26,17 +30,31 @@ _SCORE = {"softmax": 0, "sigmoid": 1}
 _fast = None
 
 
+class _NoFast:
+    """Stands in for the fast path's module: takes no call."""
+
+    @staticmethod
+    def _none(*args):
+        return None
+
+    quant_act = gemm = norm = moe = _none
+
+
 def _load_fast():
     """The fast path's module (loads the library first: it links to it)."""
     global _fast
     _lib.load()
     try:
-        from . import _binding
+        m = importlib.import_module(__package__ + "._binding")
+        why = None if getattr(m, "torch_version", None) == torch.__version__ else "was built for another PyTorch"
     except ImportError as e:
-        raise RuntimeError("_binding.so is missing or does not fit this PyTorch: build it with "
-                           "`python -m nvfp4_binary_rank_b200.build`") from e
-    _fast = _binding
-    return _binding
+        m, why = None, f"cannot be loaded ({e})"
+    if why:
+        warnings.warn(f"_binding.so {why}; the FP8 calls take several microseconds more without it: build it with "
+                      "`python -m nvfp4_binary_rank_b200.build`", RuntimeWarning, stacklevel=3)
+        m = _NoFast
+    _fast = m
+    return m
 
 
 def _done(r, fn: str):

@@ -75,13 +75,15 @@ def _build_binding(force, verbose):
     import torch
     from torch.utils import cpp_extension
 
-    src = os.path.join(CSRC, "binding.cpp")
-    newest = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "biloco.h"), torch.__file__))
-    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest:
+    src, stamp = os.path.join(CSRC, "binding.cpp"), os.path.join(OBJ, "binding.torch")
+    newest = max(os.path.getmtime(p) for p in (src, os.path.join(INCLUDE, "biloco.h")))
+    built_for = open(stamp).read() if os.path.exists(stamp) else None
+    if not force and os.path.exists(BINDING) and os.path.getmtime(BINDING) >= newest and built_for == torch.__version__:
         return
     cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f'-DBILOCO_TORCH_VERSION="{torch.__version__}"',
            *(f"-I{p}" for p in [*cpp_extension.include_paths(), cuda, sysconfig.get_paths()["include"]]),
            src, "-o", BINDING + ".tmp", f"-L{PKG}", "-l:libbiloco.so", "-Wl,-rpath,$ORIGIN",
            *(f"-L{p}" for p in cpp_extension.library_paths()), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda",
@@ -93,11 +95,19 @@ def _build_binding(force, verbose):
         sys.stderr.write(res.stdout + res.stderr)
         raise RuntimeError("the compiler failed on binding.cpp")
     os.replace(BINDING + ".tmp", BINDING)
+    with open(stamp, "w") as f:
+        f.write(torch.__version__)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     lib = _build_library(force, verbose)
-    _build_binding(force, verbose)
+    try:
+        _build_binding(force, verbose)
+    except (RuntimeError, OSError) as e:
+        # the library serves every call without it; an older one may not match the library any more
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+        sys.stderr.write(f"built without the FP8 calls' fast path: {e}\n")
     return lib
 
 

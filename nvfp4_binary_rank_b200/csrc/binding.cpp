@@ -216,4 +216,9 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__binding(void) { return PyModule_Create(&kModule); }
+PyMODINIT_FUNC PyInit__binding(void) {
+  PyObject* m = PyModule_Create(&kModule);
+  // the PyTorch whose headers this was compiled against: its tensors' layout is no other's
+  if (m && PyModule_AddStringConstant(m, "torch_version", BILOCO_TORCH_VERSION) != 0) Py_CLEAR(m);
+  return m;
+}
