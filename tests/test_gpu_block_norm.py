@@ -147,3 +147,108 @@ def test_empty_and_refusals(nb):
             nb.block_norm(**{**c, **bad})
     with pytest.raises(nb.BilocoError):
         nb.block_norm(c["y"][:, :60], c["h"][:, :60], pre_weight=w[:60])
+
+
+def verify_on_gpu(c, got, quant, res_scale=1.0, offset=0.0, eps=1e-6):
+    """verify() for many rows, in FP64 on the GPU; the same tolerances."""
+    y, h, post, g, pre = (None if c[k] is None else c[k].double() for k in ("y", "h", "post_weight", "gate", "pre_weight"))
+    M, D = (h if y is None else y).shape
+    u = torch.zeros((M, D), dtype=torch.float64, device="cuda") if y is None else y
+    if post is not None:
+        u = u / ((u * u).mean(1, keepdim=True) + eps).sqrt() * (post + offset)
+    if g is not None:
+        u = u * g.repeat_interleave(M // g.shape[0], 0)
+    ah = torch.zeros_like(u) if h is None else res_scale * h
+    h2, gu = ah + u, u.abs()
+    h_out = got if pre is None else got[0]
+    assert bool(((h_out.double() - h2).abs() <= (2.0 ** -19 + 2.0 ** -23) * gu + 2.0 ** -23 * ah.abs()
+                 + HALF[h_out.dtype] * h2.abs() * (1 + 2.0 ** -10) + 1e-38).all())
+    if pre is None:
+        return
+    rw = (pre + offset).abs() / ((h2 * h2).mean(1, keepdim=True) + eps).sqrt()
+    x = h2 / ((h2 * h2).mean(1, keepdim=True) + eps).sqrt() * (pre + offset)
+    tol = 2.0 ** -17 * (x.abs() + rw * (ah.abs() + gu))
+    if not quant:
+        assert bool(((got[1].double() - x).abs() <= tol + 2.0 ** -8 * x.abs() * (1 + 2.0 ** -10) + 1e-38).all())
+        return
+    KB = -(-D // 128)
+    pad = lambda t: torch.nn.functional.pad(t, (0, KB * 128 - D)).view(M, KB, 128)  # noqa: E731
+    amax, top, scales = pad(x.abs()).amax(2), pad(tol).amax(2), got[2].double().t()
+    assert bool(((scales - amax.clamp(min=2.0 ** -100) / 448).abs() <= (top + 2.0 ** -22 * amax) / 448 + 1e-40).all())
+    s = scales.repeat_interleave(128, 1)[:, :D]
+    assert bool(((got[1].double() * s - x).abs() <= (2.0 ** -4 * x.abs() + s * 2.0 ** -10) * (1 + 2.0 ** -10) + 2 * tol).all())
+
+
+def same(a, b):
+    a, b = ((t,) if torch.is_tensor(t) else t for t in (a, b))
+    return all(torch.equal(u.view(torch.uint8), v.view(torch.uint8)) for u, v in zip(a, b))
+
+
+# More rows than CTAs run at once, so that each walks over several: one piece a thread (D up to 1024), two
+# (up to 8192), four (above); the last rows of the walk are fewer than the CTAs.
+WALKS = [(3000, 512), (5000, 16), (2000, 1160), (3001, 5120), (1500, 8192), (700, 8208), (401, 16400)]
+
+
+@pytest.mark.parametrize("quant", [False, True])
+@pytest.mark.parametrize("h_type,w_type", [(torch.bfloat16, torch.bfloat16), (torch.float32, torch.float32)])
+@pytest.mark.parametrize("M,D", WALKS)
+def test_walks_over_rows(nb, M, D, h_type, w_type, quant):
+    if quant and D % 16:
+        D += 8
+    c = case(M, D, h_type, w_type)
+    got = nb.block_norm(**c, res_scale=0.9, quant=quant)
+    verify_on_gpu(c, got, quant, res_scale=0.9)
+    for _ in range(20):
+        assert same(got, nb.block_norm(**c, res_scale=0.9, quant=quant))
+
+
+@pytest.mark.parametrize("post,gate,pre,no_y,no_h", [
+    (False, 0, True, False, False), (True, 1, True, False, False), (True, 500, True, False, False),
+    (False, 4, False, False, False), (True, 0, False, False, False), (False, 0, True, True, False),
+    (True, 2, True, False, True), (False, 0, False, True, False), (False, 2000, True, False, False)])
+@pytest.mark.parametrize("D", [528, 2064, 8208])
+def test_walks_with_optional_parts(nb, D, post, gate, pre, no_y, no_h):
+    """One sum a row, none, and two: the barriers between rows are different ones."""
+    c = case(2000, D, torch.float32, post=post, gate=gate, pre=pre)
+    if no_y:
+        c["y"] = None
+    if no_h:
+        c["h"] = None
+    kw = dict(res_scale=1.25, offset=1.0, eps=1e-3)
+    for quant in ([False, True] if pre else [False]):
+        got = nb.block_norm(**c, **kw, quant=quant)
+        verify_on_gpu(c, got, quant, **kw)
+        for _ in range(20):
+            assert same(got, nb.block_norm(**c, **kw, quant=quant))
+
+
+@pytest.mark.parametrize("h_type", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,D", [(3000, 512), (2000, 1168), (3001, 5120), (700, 8208)])
+def test_walks_in_place_and_over_strided_rows(nb, M, D, h_type):
+    """h' over h, whose next row is loaded while this one is written; the columns beside stay."""
+    c = case(M, D, h_type, h_type, gate=1)
+    want = nb.block_norm(**c, quant=True)
+    wide_y = torch.zeros((M, D + 24), dtype=torch.bfloat16, device="cuda")
+    wide_h = torch.full((M, D + 40), 3.0, dtype=h_type, device="cuda")
+    wide_y[:, 8:8 + D] = c["y"]
+    wide_h[:, 16:16 + D] = c["h"]
+    c["y"], c["h"] = wide_y[:, 8:8 + D], wide_h[:, 16:16 + D]
+    got = nb.block_norm(**c, out_h=c["h"], quant=True)
+    assert got[0].data_ptr() == c["h"].data_ptr()
+    assert torch.equal(got[0], want[0]) and same(got[1:], want[1:])
+    assert bool((wide_h[:, :16] == 3).all()) and bool((wide_h[:, 16 + D:] == 3).all())
+
+
+@pytest.mark.parametrize("D", [512, 2064, 8208])
+def test_bad_rows_of_a_walk_spoil_only_themselves(nb, D):
+    M = 2000
+    c = case(M, D)
+    clean, cc, cs = nb.block_norm(**c, quant=True)
+    bad = torch.arange(0, M, 7, device="cuda")
+    c["y"][bad, 3] = float("nan")
+    h2, codes, scales = nb.block_norm(**c, quant=True)
+    keep = torch.ones(M, dtype=torch.bool, device="cuda")
+    keep[bad] = False
+    assert bool(h2[bad].isnan().all()) and bool(scales[:, bad].isnan().all())
+    assert torch.equal(h2[keep], clean[keep]) and torch.equal(scales[:, keep], cs[:, keep])
+    assert torch.equal(codes[keep].view(torch.uint8), cc[keep].view(torch.uint8))
