@@ -40,9 +40,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
-#include <map>
 #include <mutex>
-#include <utility>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -669,26 +667,36 @@ constexpr int kMaxDevices = 64;
 
 std::atomic<bool> g_drop_scales{false};   // failure-path self test, consumed by the next product
 
-// The status words handed out, by device.
+// The status words handed out on a device: word i is that of stream[i], i from 1 to `used`.  Fixed
+// in size, since nothing may be thrown out of a C call.
 struct StatusWords {
-  std::mutex mu;
-  std::map<std::pair<int, cudaStream_t>, int> of_stream;
-  int next[kMaxDevices] = {};
-  bool shared[kMaxDevices] = {};         // word 0 may hold something
+  cudaStream_t stream[kStatusWords];
+  int used;
+  bool shared;                           // word 0 may hold something
+  int find(cudaStream_t s) const {
+    int i = used;
+    while (i > 0 && stream[i] != s) --i;
+    return i;
+  }
 };
-StatusWords g_words;
+StatusWords g_words[kMaxDevices];
+std::mutex g_words_mu;
 
 // The word for a call on stream `s` of the current device `dev`; -1 where CUDA refuses.
 int status_word(int dev, cudaStream_t s) {
   cudaStreamCaptureStatus capture;
   if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) return -1;
-  std::lock_guard<std::mutex> lk(g_words.mu);
+  std::lock_guard<std::mutex> lk(g_words_mu);
+  StatusWords& w = g_words[dev];
   if (capture == cudaStreamCaptureStatusNone) {
-    const auto at = g_words.of_stream.find({dev, s});
-    if (at != g_words.of_stream.end()) return at->second;
-    if (g_words.next[dev] + 1 < kStatusWords) return g_words.of_stream[{dev, s}] = ++g_words.next[dev];
+    const int at = w.find(s);
+    if (at) return at;
+    if (w.used + 1 < kStatusWords) {
+      w.stream[++w.used] = s;
+      return w.used;
+    }
   }
-  g_words.shared[dev] = true;
+  w.shared = true;
   return 0;
 }
 
@@ -773,10 +781,9 @@ int fp8_take_status(cudaStream_t s) {
   int own = 0;
   bool shared = false;
   {
-    std::lock_guard<std::mutex> lk(g_words.mu);
-    const auto at = g_words.of_stream.find({dev, s});
-    if (at != g_words.of_stream.end()) own = at->second;
-    shared = g_words.shared[dev];
+    std::lock_guard<std::mutex> lk(g_words_mu);
+    own = g_words[dev].find(s);
+    shared = g_words[dev].shared;
   }
   const int status = own ? take_word(own, s) : BILOCO_OK;
   if (status != BILOCO_OK || !shared) return status;

@@ -8,6 +8,10 @@ kernel's own abort protocol runs: the waiting CTAs give up, leave together,
 drain their copies and MMAs, free their tensor memory and return; the host then
 resets the counters and the next call on the stream is correct."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -16,6 +20,7 @@ import workloads
 from gpu_common import assert_y_close, device_problem, oracle_for, y_to_numpy
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -154,6 +159,41 @@ def test_an_expired_fp8_product_in_a_graph_is_reported(nb):
         graphs[1][0].replay()
     assert nb.last_error(s) == 0
     assert torch.equal(graphs[1][1], want)
+
+
+MANY_STREAMS = """
+import ctypes, sys
+sys.path.insert(0, {root!r})
+import torch
+import nvfp4_binary_rank_b200 as nb
+x = nb.fp8_quant_act(torch.ones((3, 1024), dtype=torch.bfloat16, device="cuda"))
+w = nb.fp8_pack_weight(torch.ones((256, 1024), device="cuda"))
+want = nb.fp8_gemm(*x, *w)
+torch.cuda.synchronize()
+streams = []
+for _ in range(1100):
+    h = ctypes.c_void_p()
+    assert int(torch.cuda.cudart().cudaStreamCreate(ctypes.addressof(h))) == 0
+    streams.append(torch.cuda.ExternalStream(h.value))
+y = [nb.fp8_gemm(*x, *w, stream=s) for s in streams]
+torch.cuda.synchronize()
+assert all(torch.equal(t, want) for t in y)
+assert all(nb.last_error(s) == 0 for s in streams)
+for i, asked in ((500, 500), (1080, 1099)):
+    nb.selftest_drop_scales()
+    nb.fp8_gemm(*x, *w, stream=streams[i])
+    if i == asked:
+        assert nb.last_error(streams[i + 1]) == 0
+    assert nb.last_error(streams[asked]) == nb._lib.ERR_TIMEOUT
+    assert nb.last_error(streams[i]) == 0
+print("a thousand streams")
+"""
+
+
+def test_more_streams_than_error_words(nb):
+    """The first 1023 streams have a word each, those beyond one together."""
+    r = subprocess.run([sys.executable, "-c", MANY_STREAMS.format(root=ROOT)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "a thousand streams" in r.stdout, r.stdout + r.stderr
 
 
 def test_drop_request_is_consumed_by_one_call(nb):
