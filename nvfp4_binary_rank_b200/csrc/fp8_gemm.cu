@@ -68,7 +68,7 @@ struct Fp8GemmParams {
   int tiles_a, tiles_b;  // tiles along the MMA's rows and columns
   int split;             // CTAs of the cluster that splits K
   int y_f32;
-  int status_word;
+  int* status;           // the call's error word
   int drop;              // failure-path self test: the scales never arrive
   int vec;               // bytes of the widest aligned store of a y row: 32, 16, 8 or 2
 };
@@ -312,7 +312,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
   volatile int* const stop = &abort_flag;
   auto give_up = [&] {
     *stop = 1;
-    record_error(&g_fp8_status[p.status_word], kDevErrTimeout);
+    record_error(p.status, kDevErrTimeout);
   };
 
   // Rows form: the promoting warps take registers from the others.  Nobody takes any back
@@ -661,6 +661,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant_
 struct DeviceSetup {
   std::once_flag once;
   cudaError_t err = cudaSuccess;
+  int* words = nullptr;        // the error words there
   int clusters[9] = {};        // clusters of 1..8 parts (pairs in the rows form) resident at once
 };
 constexpr int kMaxDevices = 64;
@@ -731,6 +732,10 @@ cudaError_t launch_instance(const CUtensorMap& ta, const CUtensorMap& tb, Fp8Gem
   std::call_once(d.once, [&] {
     d.err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (d.err != cudaSuccess) return;
+    void* words = nullptr;
+    d.err = cudaGetSymbolAddress(&words, g_fp8_status);
+    if (d.err != cudaSuccess) return;
+    d.words = static_cast<int*>(words);
     cudaFuncAttributes fa;
     d.err = cudaFuncGetAttributes(&fa, kernel);
     if (d.err != cudaSuccess) return;
@@ -755,6 +760,9 @@ cudaError_t launch_instance(const CUtensorMap& ta, const CUtensorMap& tb, Fp8Gem
     }
   });
   if (d.err != cudaSuccess) return d.err;
+  const int word = status_word(dev, s);
+  if (word < 0) return cudaErrorStreamCaptureImplicit;
+  p.status = d.words + word;
   // K is split as far as all clusters still run at once: the weight's stream (or a tile's
   // chain of blocks) gets shorter with every part, a second wave costs more than it saves.
   // Measured, us at M, N, K (parts): 1, 5120, 5120: 13.3 (1), 8.1 (4), 7.7 (5), 12.7 (7, which
@@ -831,10 +839,6 @@ int run_fp8_gemm(const uint8_t* xq, const float* xs, const uint8_t* wq, const fl
   p.KB = (K + kFp8Block - 1) / kFp8Block;
   p.NB = (N + 127) / 128;
   p.y_f32 = y_f32;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return BILOCO_ERR_CUDA;
-  p.status_word = status_word(dev, s);
-  if (p.status_word < 0) return BILOCO_ERR_CUDA;
   p.drop = g_drop_scales.exchange(false);
   const unsigned long long bits = reinterpret_cast<uintptr_t>(y) | static_cast<unsigned long long>(N) * (y_f32 ? 4 : 2);
   p.vec = bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : bits % 8 == 0 ? 8 : 2;
