@@ -331,6 +331,18 @@ def test_a_weight_packed_just_before_its_product(nb, M):
 
 
 @pytest.mark.parametrize("M", [1, 50, 400])
+def test_a_weight_copied_just_before_its_product(nb, M):
+    N, K = 1024, 1040
+    sets = [operands(nb, np.random.default_rng(20 + i), M, N, K) for i in range(3)]
+    want = [nb.fp8_gemm(*s) for s in sets]
+    mine = [t.clone() for t in sets[0]]
+    for i in range(150):
+        for k in (0, 1, 3, 2):
+            mine[k].copy_(sets[i % 3][k])
+        assert torch.equal(nb.fp8_gemm(*mine), want[i % 3])
+
+
+@pytest.mark.parametrize("M", [1, 50, 400])
 def test_streams_and_graphs(nb, M):
     """Two calls at once on two streams, and a captured quantise + product replayed on new inputs."""
     N, K = 1024, 1040

@@ -236,6 +236,34 @@ def test_two_streams_and_two_graphs_at_once(nb, T, k, shared):
         assert all(torch.equal(u, v) for u, v in zip(out, w))
 
 
+@pytest.mark.parametrize("T", [1, 20])
+def test_operands_written_just_before_the_layer(nb, T):
+    """router and w2 are read early; PyTorch's kernels and the packer right in front come first all the same."""
+    layers = [layer(nb, T, 512, 256, 16, seed=s)[0] for s in range(3)]
+    g = torch.Generator(device="cuda").manual_seed(1)
+    raw = [torch.randn((16, 512, 256), generator=g, device="cuda") for _ in layers]
+    want = []
+    for p, r in zip(layers, raw):
+        p["w2"], p["w2_scales"] = nb.fp8_pack_weight(r)
+        torch.cuda.synchronize()
+        want.append(nb.fp8_moe(**p, top_k=4))
+        torch.cuda.synchronize()
+    q = {k: v.clone() for k, v in layers[0].items()}
+    for i in range(150):
+        j = i % 3
+        for k in ("x", "w13", "w13_scales", "w2", "w2_scales", "router"):
+            q[k].copy_(layers[j][k])
+        assert all(torch.equal(a, b) for a, b in zip(want[j], nb.fp8_moe(**q, top_k=4)))
+    del q["w2"], q["w2_scales"]
+    for i in range(150):                     # the same memory for every packed weight
+        j = i % 3
+        for k in ("x", "w13", "w13_scales", "router"):
+            q[k].copy_(layers[j][k])
+        w2, s2 = nb.fp8_pack_weight(raw[j])
+        got = nb.fp8_moe(**q, w2=w2, w2_scales=s2, top_k=4)
+        assert all(torch.equal(a, b) for a, b in zip(want[j], got))
+
+
 @pytest.mark.parametrize("T", [1, 33])
 def test_a_bias_of_minus_infinity_leaves_an_expert_out(nb, T):
     """Masked experts are picked only where nothing else is left, and then the lowest first."""
