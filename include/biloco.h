@@ -264,7 +264,8 @@ int biloco_gemm_noalloc(const void *x_bf16, const uint8_t *W_fp4, const uint8_t 
 /*
  * ---- FP8 block format -----------------------------------------------------
  * The layers of a model that stay at 8 bits next to the NVFP4 ones, and the steps
- * between them.  The BiLoCo pages have no counterpart of these calls.
+ * between them, for inference: none has a backward pass.  The BiLoCo pages have no
+ * counterpart of these calls.
  *
  * Format: E4M3 codes (sign, 4 exponent, 3 mantissa bits; 0x7F and 0xFF are NaN) with
  * one FP32 scale per 128 elements of a row (activations) or per 128 x 128 tile
@@ -306,9 +307,13 @@ int biloco_fp8_pack_weight(const void *W, int w_type, int E, int N, int K, uint8
  *           16 <= K <= 2^24; codes 16-byte aligned
  * Any batch size runs one kernel, which keeps no scratch and shares nothing between
  * calls: calls on different streams, and graphs replayed at once, do not disturb each
- * other.  Sums are FP32; the result depends only on the operands and the shape.
+ * other.  Sums are FP32; the result depends only on the operands, the shape and the GPU
+ * (K is split by how many clusters of CTAs it holds at once).  The product of two scales
+ * is formed first, in FP32: beyond 2^128 it is infinite, below 2^-126 it loses bits.
  * The kernel is launched with programmatic dependent launch and reads w_codes before it
- * waits for the kernel before it (see biloco_gemm on what must not write the weight).
+ * waits for the kernel before it (see biloco_gemm on what must not write the weight: of
+ * this library's calls only the packers may have written it since the last kernel of
+ * another origin on the stream).
  * A bounded wait that expires inside the kernel is reported by biloco_last_error on the
  * call's stream; y is then not valid.  That of a call captured into a graph, or on a
  * stream beyond the first 1023 that made such calls on the device, is reported on whichever
@@ -333,6 +338,7 @@ int biloco_fp8_gemm(const uint8_t *x_codes, const float *x_scales, const uint8_t
  *   x_bf16       out [M][D] bfloat16, or NULL
  *   codes,scales out x as FP8 blocks (D % 16 == 0), layout of biloco_fp8_quant_act, or NULL
  * h' enters x unrounded, and x the FP8 blocks unrounded: each output is rounded once.
+ * A row's FP32 sums may be added in another order in a batch of another size.
  * limits: 0 <= M <= 2^30, 8 <= D <= BILOCO_NORM_MAX_D, D % 8 == 0, row strides >= D and multiples of 8
  * elements, 16-byte aligned arrays.  Outputs must not overlap inputs other than h_out = h
  * with the same stride.
@@ -362,14 +368,18 @@ int biloco_block_norm(const void *y_bf16, long long ldy, const void *h, long lon
  *            use after it.  Two calls that may overlap need two of them.
  *   limits   0 <= T <= 64 (0: nothing is done), D and F multiples of 16 up to 16384,
  *            1 <= k <= 16, k <= E <= 512, 0 <= shared <= 4
- * Scores are summed to better than FP32 and compared in FP64; a score that is not a number
- * is picked last.  The products are FP16 x E4M3 with FP32 sums: rows of x are scaled into
- * FP16 exactly (BF16 values more than 2^29 below the row's largest lose bits), the hidden
- * values are rounded to FP16.  A token with an infinity or NaN spoils only its own row.
+ * Scores are FP32 sums of eight products each, added with compensation and then in FP64, and
+ * compared in FP64; a score that is not a number is picked last.  The products are FP16 x E4M3
+ * with FP32 sums (weight scales up to 2^88 keep them finite): rows of x are scaled into FP16
+ * exactly (BF16 values more than 2^29 below the row's largest lose bits).  The hidden values
+ * are rounded to FP16's 11 bits, where FP32 would hold 24: with a BF16 output the error against
+ * an exact layer grows by about 1% (0.00165 to 0.00167 of the output's size).  Those below 2^-28
+ * of a token's and expert's largest lose more bits, and below 2^-38 they vanish.  A token with
+ * an infinity or NaN spoils only its own row.
  * Four kernels (three for one token) with programmatic dependent launch; router and w2 may be
  * read before the kernel before them on the stream has ended (see biloco_gemm on what must
- * not write the weight).
- * The result depends only on the operands and the shape.
+ * not write the weight: the same as for biloco_fp8_gemm's).
+ * The result depends only on the operands, the shape and the GPU (the number of its SMs).
  */
 #define BILOCO_MOE_MAX_T 64
 #define BILOCO_MOE_MAX_D 16384

@@ -1,5 +1,7 @@
 """Binding of the FP8 block-format operators and the block norm (include/biloco.h).
 
+Inference only: operands that require a gradient are taken, and the outputs carry none.
+
 Argument checks and marshalling only.  Outputs are allocated on the stream the call
 runs on, and the call runs on its tensors' device whatever the current one is.
 
@@ -104,7 +106,7 @@ def _rows_ok(t, dtype, dev) -> bool:
 
 def fp8_quant_act(x: torch.Tensor, stream=None):
     """BF16 [M, K] (rows contiguous, any row stride that is a multiple of 8) ->
-    (codes float8_e4m3fn [M, K], scales float32 [ceil(K/128), M])."""
+    (codes float8_e4m3fn [M, K], scales float32 [ceil(K/128), M]), without a gradient."""
     if stream is None:
         r = (_fast or _load_fast()).quant_act(x)
         if r is not None:
@@ -126,7 +128,7 @@ def fp8_quant_act(x: torch.Tensor, stream=None):
 
 def fp8_pack_weight(W: torch.Tensor, stream=None):
     """BF16 or float32 [N, K] or [E, N, K] -> (codes float8_e4m3fn of W's shape,
-    scales float32 [(E,) ceil(N/128), ceil(K/128)])."""
+    scales float32 [(E,) ceil(N/128), ceil(K/128)]), without a gradient."""
     dev = W.get_device() if isinstance(W, torch.Tensor) else -1
     if dev < 0 or W.dtype not in _TYPE or W.dim() not in (2, 3) or not W.is_contiguous():
         _refuse(dev, (W, "W", (_BF16, _F32), (None,) * (3 if isinstance(W, torch.Tensor) and W.dim() == 3 else 2)))
@@ -145,9 +147,9 @@ def fp8_pack_weight(W: torch.Tensor, stream=None):
 def fp8_gemm(x_codes: torch.Tensor, x_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
              out: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16, stream=None) -> torch.Tensor:
     """y[m, n] = sum_b x_scales[b, m] w_scales[n/128, b] (x[m] . w[n])_b over blocks b of 128
-    along K, for any number of rows; y is bfloat16 or float32.  w_codes may be read while the kernel
-    before this one on the stream still runs: no call of this library but fp8_pack_weight may have
-    written it just before."""
+    along K, for any number of rows; y is bfloat16 or float32 and carries no gradient.  w_codes
+    may be read while earlier calls of this library on the stream still run: none of them but
+    fp8_pack_weight may have written it since PyTorch's last kernel there."""
     if stream is None and (out is not None or out_dtype in _TYPE):
         r = (_fast or _load_fast()).gemm(x_codes, x_scales, w_codes, w_scales, out,
                                          (out_dtype if out is None else getattr(out, "dtype", None)) is _F32)
@@ -205,8 +207,8 @@ def block_norm(y: torch.Tensor | None, h: torch.Tensor | None, *, post_weight: t
     y is bfloat16 [M, D] (None: no block before, u = 0), h bfloat16 or float32 [M, D]
     (None: no residual yet; h' is then bfloat16), gate [D] or [G, D] with M % G == 0
     (each row serves M / G consecutive rows).  Returns (h', x), (h', codes, scales) with
-    `quant` (as fp8_quant_act lays them out), or h' alone without pre_weight.  out_h may
-    be h itself."""
+    `quant` (as fp8_quant_act lays them out), or h' alone without pre_weight; none carries a
+    gradient.  out_h may be h itself, and must not overlap the inputs otherwise."""
     if stream is None and out_h is None:
         r = (_fast or _load_fast()).norm(y, h, post_weight, pre_weight, gate, res_scale, offset, eps, bool(quant))
         if r is not None:
@@ -292,9 +294,10 @@ def fp8_moe(x: torch.Tensor, router: torch.Tensor, w13: torch.Tensor, w13_scales
     and w2 [n, D, F] with their scales from fp8_pack_weight.  The n - E last experts are
     shared: they serve every token with weight 1.  `score` is "softmax" (over the experts)
     or "sigmoid"; bias float32 [E] is added for the choice only.  Returns (y bfloat16
-    [T, D], ids int32 [T, top_k], weights float32 [T, top_k]).  router and w2 may be read while the
-    kernel before this call on the stream still runs: no call of this library but fp8_pack_weight
-    may have written them just before."""
+    [T, D], ids int32 [T, top_k], weights float32 [T, top_k]), none with a gradient.  The hidden
+    values are held in FP16.  router and w2 may be read while earlier calls of this library on the
+    stream still run: none of them but fp8_pack_weight may have written them since PyTorch's last
+    kernel there."""
     if stream is None and score in _SCORE:
         r = (_fast or _load_fast()).moe(x, router, w13, w13_scales, w2, w2_scales, bias, top_k, _SCORE[score], bool(renorm),
                                         route_scale)

@@ -11,9 +11,13 @@
 // 696 instructions a warp and row and was bound by them).  CTAs stay: each walks over rows,
 // and the loads of its next row are under way from the middle of the current one, when the
 // registers of that are free.  y and h pass by L1, which so keeps the weights.
-// Measured at 8192 x 5120 with FP8 output (295 MB): one CTA per row 85 us, this 65 us (4.5 TB/s,
-// instructions issued in 70% of the clocks); one row of 5120 takes 3.0 us, two reductions over a
-// CTA and the loads before them.
+// Measured at 8192 x 5120 with FP8 output (295 MB): one CTA per row 85 us, this 63 to 66 us (4.5 TB/s,
+// instructions issued in 65% of the clocks); with BF16 output (336 MB) 61 us, 5.5 TB/s.  Neither
+// memory nor the issue slots are full: a row waits for two sums over its CTA, and three rows
+// are under way on an SM.  One row of 5120 takes 2.5 to 3.0 us, the two sums and the loads before them.
+// Rows above 8192 (four pieces a thread, one CTA of 1024 an SM at 64 registers, 200 to 372 bytes of
+// them spilled): 2048 x 16384 in 76 us with FP8 and 69 us with BF16 output, 1024 x 32768 in 82 and 75
+// (floors 36 and 41).
 // Both sums of squares are FP32; x is computed from the unrounded h', so h' and x are each
 // rounded once.
 #include <algorithm>
@@ -268,7 +272,7 @@ template <int kVec, int kMaxThreads, bool kHf32, bool kWf32>
 cudaError_t launch_one(const BlockNormArgs& a, cudaStream_t s) {
   auto kernel = block_norm_kernel<kVec, kMaxThreads, kHf32, kWf32>;
   const int nvec = a.D / 8, warps = ((nvec + kVec - 1) / kVec + 31) / 32;
-  // as many CTAs as run at once, at most one per row
+  // as many CTAs as run at once, at most one per row; every GPU this library takes holds as many an SM
   static std::atomic<int> per_sm[kMaxThreads / 32 + 1];
   int n = per_sm[warps].load();
   if (n == 0) {

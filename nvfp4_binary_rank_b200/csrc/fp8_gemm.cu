@@ -18,16 +18,21 @@
 //     its columns tokens, so a decode batch is not padded to 128 rows; scales vary over the
 //     columns.  Bound by reading the weight.
 // Measured, device time past L2 (M tokens, N x K weight):
-//   4096, 13824 x 5120: 265 us, 2.19 PFLOP/s.  A block of 128 takes about 790 clocks, of which its
-//     MMAs are 513; the rest is the chain commit - read back - release of an accumulator.  Runs
-//     of seconds are held by the power limit at about 310 us.
-//   512, 5120 x 5120: 23.5 us;  333, 1000 x 2064: 9.2 us (latency of one chain of blocks)
-//   1, 5120 x 5120: 8.6 us, 3.1 TB/s;  16, 13824 x 5120: 15.3 us, 4.7 TB/s: each CTA's part of
-//     the weight is a few blocks, so starting up and joining the parts weigh as much as the stream.
-// What was slower: rows form with one accumulator pair of 256 columns (275 us at 4096 tokens, 29.0
-// at 512), without a pair of CTAs (128 x 256 tiles: 308), without moving registers (278), with
-// eight promoting warps (279); swapped form with three smaller CTAs an SM (1 token 9.1 us, 16
-// tokens 17.1).
+//   4096, 13824 x 5120: 269 us, 2.16 PFLOP/s, in runs of tens of milliseconds (466 thousand clocks
+//     at 1.6 to 1.75 GHz); 310 to 320 us, 1.8 to 1.9 PFLOP/s, in runs of seconds, which the power
+//     limit holds at 1.4 to 1.5 GHz.  A block of 128 takes 846 clocks, of which its MMAs are 513; the
+//     rest is the chain commit - read back - release of an accumulator.  A tile's beginning and end
+//     are 5000 clocks, 13% of its time at 40 blocks.
+//   512, 5120 x 5120: 23.4 us, 40 tiles on 74 pairs;  2048: 72 us, 160 tiles in three rounds
+//   129, 5120 x 5120: 16.3 us, 20 tiles in three parts;  333, 1000 x 2064: 9.1 us (latency of one
+//     chain of blocks)
+//   1, 5120 x 5120: 8.6 us, 3.1 TB/s, 40 tiles in three parts of 13 and 14 blocks: starting up and
+//     joining the parts weigh as much as the stream
+//   16, 13824 x 5120: 15.2 us, 4.7 TB/s: 108 tiles, K not split, 40 SMs without work
+// What was slower, where the kept form took 265 us at 4096 tokens: rows form with one accumulator
+// pair of 256 columns (275 us at 4096 tokens, 29.0 at 512), without a pair of CTAs (128 x 256 tiles:
+// 308), without moving registers (278), with eight promoting warps (279); swapped form with three
+// smaller CTAs an SM (1 token 9.1 us, 16 tokens 17.1).
 // The token scales come through a ring in shared memory that a warp of its own fills a few
 // blocks ahead: loaded by the promoting warps themselves, one block ahead, their latency
 // (about 1000 clocks under load) set the pace of the rows form.
@@ -35,7 +40,8 @@
 // Where there are fewer tiles than CTA slots, a cluster of up to 8 CTAs splits K: each
 // leaves its FP32 sums in its own shared memory and the cluster adds them in rank order
 // over distributed shared memory, so the result does not depend on timing and no
-// workspace or counter outlives the call.
+// workspace or counter outlives the call.  CTA slots are what the device query counts: one
+// CTA an SM, for the smaller tiles of the swapped form too, whatever their shared memory.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -758,10 +764,11 @@ cudaError_t launch_instance(const CUtensorMap& ta, const CUtensorMap& tb, Fp8Gem
   const int word = status_word(dev, s);
   if (word < 0) return cudaErrorStreamCaptureImplicit;
   p.status = d.words + word;
-  // K is split as far as all clusters still run at once: the weight's stream (or a tile's
-  // chain of blocks) gets shorter with every part, a second wave costs more than it saves.
-  // Measured, us at M, N, K (parts): 1, 5120, 5120: 13.3 (1), 8.1 (4), 7.7 (5), 12.7 (7, which
-  // does not fit); 129, 5120, 5120: 24.2 (1), 16.3 (3), 27.1 (4, does not fit).
+  // K is split as far as all clusters still run at once, by the device's count (148 of one CTA, 74,
+  // 45, 33, 26, 22, 15 and 15 of eight in the swapped form; 74 of one pair, 33, 22 and 15 in the rows
+  // form): the weight's stream (or a tile's chain of blocks) gets shorter with every part, a second
+  // wave costs more than it saves.  Measured, us at M, N, K (parts): 1, 5120, 5120: 13.3 (1), 8.6
+  // (3); 129, 5120, 5120: 24.2 (1), 16.3 (3), 27.1 (4, does not fit).
   const long long tiles = static_cast<long long>(p.tiles_a) * p.tiles_b;
   int split = 1;
   for (int q = 2; q <= kMaxSplit && q <= p.KB; ++q)
@@ -799,7 +806,8 @@ int fp8_take_status(cudaStream_t s) {
 // give a small problem more CTAs, and parts of K; large ones read the weight fewer times.  The
 // estimate, in units of one block's time in a tile of 128: the blocks of a CTA (as many as its SM
 // holds share it) and 7 for the rest, of which a tile of up to 32 columns takes 0.6, and the
-// operands of all tiles at 25 MB.  Measured, us with 32, 64, 128 columns: 5.3, 6.1, 7.9 (128 tokens,
+// operands of all tiles at 25 MB.  It is a fit to measured times, with two CTAs an SM up to 64
+// columns; how K is split is decided by the device's count at the launch.  Measured, us with 32, 64, 128 columns: 5.3, 6.1, 7.9 (128 tokens,
 // 512 x 2064), 7.6, 8.8, 9.3 (64, 2048 x 5120), 10.2, 10.0, 10.3 (128, 2048 x 5120), 15.5, 11.8, 12.6 (64,
 // 5120 x 5120), 25.7, 21.1, 13.5 (128, 5120 x 5120), 15.9, 13.5, 10.7 (333, 1024 x 5120).
 static int swapped_columns(int M, int NB, int KB) {

@@ -4,14 +4,16 @@
 //   y[t] = sum over its experts e of w_e * W2_e (silu(W1_e x) * (W3_e x)),  W13 = [W1; W3]
 //
 // With few tokens the layer is the stream of the picked experts' weights: 3 D F bytes for
-// each of them, everything else is small.  So every weight byte is read once, straight into
-// the registers that feed the multiplication (a warp's 16-byte loads cover eight rows of 64
-// bytes), and the tokens of an expert share it.  The products run on the warp-level tensor
-// instruction (m16n8k16, FP16 operands, FP32 sums): at up to 16 tokens per expert it needs
-// about a third of its rate, where a tcgen05 tile would first have to go through shared
-// memory.  E4M3 values are exact in FP16.  The activations are not quantised: a token's row
-// is scaled by a power of two into FP16's range, which is exact for BF16 values down to
-// 2^-29 of the row's largest, and the hidden row keeps FP16's 11 bits.
+// each of them, everything else is small.  So every weight byte is read from memory once, through
+// a ring in shared memory that belongs to the warp that multiplies it (a warp's 16-byte copies
+// cover eight rows of 64 bytes), and up to 16 tokens of an expert share it; further tokens of the
+// expert read it from L2 again.  The products run on the warp-level tensor instruction (m16n8k16,
+// FP16 operands, FP32 sums): at up to 16 tokens per expert it needs about a third of its rate,
+// where a tcgen05 tile of 128 rows would need a layout of its own in shared memory, and a block's
+// scales applied behind it.  E4M3 values are exact in FP16.  The activations are not quantised: a
+// token's row is scaled by a power of two into FP16's range, which is exact for BF16 values down to
+// 2^-29 of the row's largest.  The hidden row keeps FP16's 11 bits, since the instruction takes
+// both operands in one type: that adds about 1% to the error of a BF16 output.
 //
 // Within a block of 128 along K the order of the terms is free, so lane t of a quad takes 16
 // consecutive elements of a 64-element run for both operands and no data is exchanged.
@@ -442,9 +444,11 @@ __device__ __forceinline__ void scale_hidden(uint32_t (&v)[8], int2 e, int row_e
 // kOne (down, one token): a cluster of the token's experts owns 64 output rows; the shares meet
 // in distributed shared memory and there is no combine kernel.
 //
-// Measured, device time past L2: 64 tokens, 65 experts of 3 x 5120 x 2048 (2.05 GB): 409 us for
-// the layer, 5.0 TB/s of weights; 16 tokens, 24 of 32 and one shared expert of 3 x 4096 x 2048
-// (0.63 GB): 134 us, 4.7 TB/s.  Bound by the latency of the loads: 16 warps an SM, each with 4 KB
+// Measured, device time past L2: 64 tokens, 65 experts of 3 x 5120 x 2048 (2.05 GB): 411 us for
+// the layer, 5.0 TB/s of weights, in runs of tens of milliseconds, 450 to 460 us in runs of seconds,
+// which the power limit holds at 1.65 GHz; 16 tokens, 24 of 32 and one shared expert of 3 x 4096 x 2048
+// (0.63 GB): 139 us, 4.5 TB/s; 64 tokens, all on each of 8 experts of 3 x 5120 x 2048 (0.25 GB, floor
+// 39 us): 230 us, four units an expert, whose conversion to FP16 and activations are each unit's own.  Bound by the latency of the loads: 16 warps an SM, each with 4 KB
 // of weights on the way, leave the schedulers idle for 60% of the time.  One token, 8 experts of
 // 3 x 2048 x 1024: 26 us, of which 14 are there without the weights, in the chain of three kernels:
 // 5 us in the router (2.4 of them for the choice), 3 and 2 us in the first pass of the products,
