@@ -446,8 +446,8 @@ __device__ __forceinline__ void scale_hidden(uint32_t (&v)[8], int2 e, int row_e
 //
 // Measured, device time past L2: 64 tokens, 65 experts of 3 x 5120 x 2048 (2.05 GB): 411 us for
 // the layer, 5.0 TB/s of weights, in runs of tens of milliseconds, 450 to 460 us in runs of seconds,
-// which the power limit holds at 1.65 GHz; 16 tokens, 24 of 32 and one shared expert of 3 x 4096 x 2048
-// (0.63 GB): 139 us, 4.5 TB/s; 64 tokens, all on each of 8 experts of 3 x 5120 x 2048 (0.25 GB, floor
+// which the power limit holds at 1.65 GHz; 16 tokens, 23 of 32 and one shared expert of 3 x 4096 x 2048
+// (0.60 GB): 127 us, 4.8 TB/s; 64 tokens, all on each of 8 experts of 3 x 5120 x 2048 (0.25 GB, floor
 // 39 us): 230 us, four units an expert, whose conversion to FP16 and activations are each unit's own.  Bound by the latency of the loads: 16 warps an SM, each with 4 KB
 // of weights on the way, leave the schedulers idle for 60% of the time.  One token, 8 experts of
 // 3 x 2048 x 1024: 26 us, of which 14 are there without the weights, in the chain of three kernels:
